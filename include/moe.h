@@ -24,7 +24,7 @@
  *     launched.  Errors found by a kernel (an expert id out of range, a pipeline wait that
  *     timed out) are OR-ed into a status word inside `ws`; read it with
  *     moe_get_device_status().  No kernel traps.
- *   - Base pointers of bf16 / e4m3 matrices must be 16-byte aligned (e2m1 weights:
+ *   - Base pointers of bf16 / e4m3 / int8 matrices must be 16-byte aligned (e2m1 weights:
  *     32-byte); H and I must be multiples of 128.
  *   - "FP8" below means both dtypes with e4m3 activations (MOE_DTYPE_FP8_E4M3 and
  *     MOE_DTYPE_FP8_FP4).
@@ -42,8 +42,15 @@
  *     base pointers 32-byte aligned, with one UE8M0 scale (2^(byte-127)) per row and 32
  *     consecutive K elements, passed as the atoms moe_prepare_fp4_scales() makes.  No
  *     shared expert, block_m 128.
+ *     dtype MOE_DTYPE_INT8: x is int8 [T,H] with one fp32 scale per token, x_scale [T]; expert
+ *     weights are int8 with one fp32 scale per output channel ([E,I] for gate/up, [E,H] for
+ *     down), each value the code times its scale; sums are exact in 32-bit integers; h is
+ *     re-quantised to int8 with one scale per row (max|h| / 127); W_r stays bf16; the output
+ *     is bf16.  No shared expert, block_m 128, H and I at most 131071.  A row of h with a NaN
+ *     or an infinity makes that row's outputs NaN.
  *   - Weight scale arguments (void*): fp32 block scales for MOE_DTYPE_FP8_E4M3, prepared
- *     atoms for MOE_DTYPE_FP8_FP4, ignored (may be NULL) for MOE_DTYPE_BF16.
+ *     atoms for MOE_DTYPE_FP8_FP4, fp32 channel scales for MOE_DTYPE_INT8, ignored (may be
+ *     NULL) for MOE_DTYPE_BF16.
  *   - Empty batch: T = 0 is valid.  After the parameter and workspace checks every call
  *     returns MOE_OK, and arrays with a T or T*K dimension are not touched (they may be
  *     NULL).  Outputs sized by E still describe the empty batch: moe_permute writes
@@ -81,7 +88,9 @@ typedef enum moe_status {
                                     /* |y| = 65504                                          */
 
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
-enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP8_E4M3 = 1, MOE_DTYPE_FP8_FP4 = 2 };
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP8_E4M3 = 1, MOE_DTYPE_FP8_FP4 = 2, MOE_DTYPE_INT8 = 3 };
+/* Output types of moe_linear_int8. */
+typedef enum moe_out_type { MOE_OUT_BF16 = 0, MOE_OUT_FP16 = 1, MOE_OUT_FP32 = 2 } moe_out_type_t;
 
 typedef struct moe_params {
   int32_t T;            /* tokens                                                        */
@@ -96,7 +105,7 @@ typedef struct moe_params {
   int32_t renormalize;  /* 1: divide the chosen weights by their sum                     */
   float routed_scale;   /* factor applied to the (renormalised) weights                  */
   int32_t I_shared;     /* intermediate size of the shared expert, 0 = none              */
-  int32_t dtype;        /* MOE_DTYPE_BF16, MOE_DTYPE_FP8_E4M3 or MOE_DTYPE_FP8_FP4       */
+  int32_t dtype;        /* MOE_DTYPE_BF16, _FP8_E4M3, _FP8_FP4 or _INT8                  */
   int32_t block_m;      /* row alignment of each expert's bucket: 128 (one-SM GEMM tiles), */
                         /* 256 (two-SM cta_group::2 tiles: a third less SM-side operand  */
                         /* traffic, more pad rows), 0 = default (128)                    */
@@ -127,6 +136,10 @@ size_t moe_workspace_size(const moe_params_t* p);
  * outputs.  0 if the parameters are invalid. */
 size_t moe_workspace_size_host(const moe_params_t* p);
 
+/* Bytes of workspace moe_norm_layer_forward() needs: moe_workspace_size() plus the normed
+ * input.  0 if the parameters are invalid. */
+size_t moe_workspace_size_norm(const moe_params_t* p);
+
 /* Bucket alignment the calls use for these parameters (128 or 256); -1 if invalid. */
 int32_t moe_effective_block_m(const moe_params_t* p);
 
@@ -136,13 +149,35 @@ int32_t moe_effective_block_m(const moe_params_t* p);
 int64_t moe_max_padded_rows(const moe_params_t* p);
 
 /* ---------------------------------------------------------------------------------- */
+/* Before the layer — residual addition and root-mean-square norm, in the layer's input  */
+/* format.  (The pages draw the norm in front of the router, "MoE" §0, and give no       */
+/* formula; the 8-bit formats are the ones that the layer's dtypes read.)                */
+/*   z   = bf16(x + residual)              (z = x when residual is NULL)                 */
+/*   y   = z / sqrt(mean_h(z^2) + eps) * norm_w                                          */
+/*   out = y by p->dtype: bf16 [T,H] (out_scale unused); e4m3 codes with out_scale       */
+/*         [T,H/128] = 2^ceil(log2(amax/448)) of the 128 channels; int8 codes with         */
+/*         out_scale [T] = amax/127 of the token, code = y / scale to the nearest, ties to  */
+/*         even (scale 1 where amax = 0, and never below 2^-126)                           */
+/*   x, residual, residual_out [T,H], norm_w [H] bf16; eps a positive normal number      */
+/* z is written to residual_out unless that is NULL; it may be residual itself, or x.    */
+/* Out may be x for the bf16 format without a residual.  Buffers that overlap otherwise  */
+/* are not supported.  Statistics in fp32 and fp64, one rounding.  In the 8-bit formats a */
+/* token with a NaN, an infinity or squares whose sum passes fp32's range gets codes 0   */
+/* and scale NaN.  Only p's T, H and dtype matter (the others must be valid).            */
+/* ---------------------------------------------------------------------------------- */
+moe_status_t moe_add_rms_norm(const moe_params_t* p, const void* x, const void* residual,
+                              const void* norm_w, float eps, void* residual_out, void* out,
+                              float* out_scale, void* stream);
+
+/* ---------------------------------------------------------------------------------- */
 /* Stage 1 — routing.  Routing primer §三 (router, scores), §四 (top-k, renormalise),   */
 /* §六-§十 (group-limited top-k); "MoE" §0 (selection-only bias).                      */
-/*   x        [T,H] bf16, or e4m3 codes with x_scale [T,H/128] (FP8 dtype)              */
+/*   x        [T,H] bf16, e4m3 codes with x_scale [T,H/128] (FP8), or int8 codes with   */
+/*            x_scale [T] (INT8: the codes enter the product, the scale the logits)     */
 /*   w_r      [E,H] bf16;  bias [E] fp32 or NULL                                        */
 /*   topk_ids [T,K] int32 out: experts in descending selection score (ties: lower id)   */
 /*   topk_w   [T,K] fp32 out: weights from the unbiased scores                          */
-/* Uses ws for the logits (and, for FP8, a bf16 copy of x).                            */
+/* Uses ws for the logits (and, for FP8 and INT8, a bf16 copy of x).                   */
 /* ---------------------------------------------------------------------------------- */
 moe_status_t moe_route(const moe_params_t* p, const void* x, const float* x_scale,
                        const void* w_r, const float* bias, int32_t* topk_ids, float* topk_w,
@@ -170,7 +205,8 @@ moe_status_t moe_aux_free_bias_update(const int32_t* counts, int32_t E, float ga
 /*   row_of_pair    [T*K] int32 out                                                     */
 /*   pair_of_row    [moe_max_padded_rows] int32 out: pair of each row, -1 on pad rows   */
 /*   x_perm         [moe_max_padded_rows, H] out: x[t] copied to each pair's row, pad   */
-/*                  rows zero (bf16, or e4m3 codes + x_perm_scale [rows, H/128] fp32)   */
+/*                  rows zero (bf16, e4m3 codes + x_perm_scale [rows, H/128] fp32, or   */
+/*                  int8 codes + x_perm_scale [rows] fp32); pad rows' scales 1          */
 /* An id outside [0,E) sets MOE_DEV_BAD_EXPERT_ID and that pair is left out.            */
 /* Masked layout (masked_cap > 0): offsets_padded[e] = e*cap; counts[e] = rows in use,  */
 /* min(pairs of e, cap); a pair past cap gets row_of_pair = -1 (MOE_DEV_CAPACITY); the  */
@@ -211,9 +247,9 @@ moe_status_t moe_permute_noalloc(const moe_params_t* p, const int32_t* topk_ids,
 /*                  Masked layout: counts (the rows in use of each expert) is required   */
 /*                  and offsets_padded may be NULL (then e*cap); 128-row tiles wholly    */
 /*                  past counts[e] are skipped by every kernel                           */
-/*   y_perm [moe_max_padded_rows, H] out, fp32 for MOE_DTYPE_BF16 and bf16 for FP8; rows */
+/*   y_perm [moe_max_padded_rows, H] out, fp32 for MOE_DTYPE_BF16, bf16 for FP8, INT8; rows */
 /*                  past counts[e] in a bucket are not written when counts is given     */
-/* The SwiGLU intermediate h (bf16, or e4m3 + scales) lives in ws.  For bf16 workloads  */
+/* The SwiGLU intermediate h (bf16, or 8-bit codes + scales) lives in ws.  For bf16 workloads  */
 /* y_perm stays fp32 because it feeds the output directly and the final bf16 rounding   */
 /* already uses most of the 2e-2 RMS error budget; the FP8 bound (6e-2) leaves room for */
 /* a bf16 y_perm, which halves its HBM round trip.                                      */
@@ -232,9 +268,27 @@ moe_status_t moe_shared_expert_ffn(const moe_params_t* p, const void* x, const v
                                    void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------- */
+/* Matrix product of 8-bit integers, the dense form of the int8 experts' products (for   */
+/* the projections and dense feed-forward networks around the layer):                    */
+/*   out[m,n] = a_scale[m] w_scale[n] sum_k a[m,k] w[n,k]  (+ bias[n])                   */
+/*   a [M,K] int8, rows lda bytes apart; a_scale [M] fp32 (as moe_add_rms_norm writes);   */
+/*   w [N,K] int8 (nn.Linear), rows ldw bytes apart; w_scale [N] fp32; bias [N] fp32 or   */
+/*   NULL; out [M,N] of out_type (moe_out_type_t), rows ldo elements apart; columns past  */
+/*   N are not touched.  The sum is exact; one rounding to out_type (fp16: to infinity    */
+/*   past 65504).                                                                        */
+/* M >= 0, N >= 1 of any size; K a multiple of 16, 16..131056; lda and ldw multiples of   */
+/* 16; a and w 16-byte aligned.  No workspace.  device_status: optional device int32 that */
+/* the caller has zeroed; MOE_DEV_TIMEOUT is OR-ed into it.                               */
+/* ---------------------------------------------------------------------------------- */
+moe_status_t moe_linear_int8(int32_t M, int32_t N, int32_t K, const void* a, int64_t lda,
+                             const float* a_scale, const void* w, int64_t ldw,
+                             const float* w_scale, const float* bias, void* out, int64_t ldo,
+                             int32_t out_type, int32_t* device_status, void* stream);
+
+/* ---------------------------------------------------------------------------------- */
 /* Stage 4 — combine (routing primer §5.3): out[t] = sum_k w[t,k] y_perm[row_of_pair[   */
 /* t*K+k]] (+ y_shared[t]), fp32 accumulation in fixed k order, one rounding to bf16.   */
-/* y_perm [rows,H] as moe_expert_ffn writes it (fp32, or bf16 for FP8); y_shared [T,H]  */
+/* y_perm [rows,H] as moe_expert_ffn writes it (fp32; bf16 for FP8, INT8); y_shared [T,H] */
 /* fp32 or NULL; out [T,H] bf16.  Pairs                                                 */
 /* with row_of_pair = -1 are left out.  No atomics: bitwise reproducible.               */
 /* ---------------------------------------------------------------------------------- */
@@ -260,7 +314,21 @@ moe_status_t moe_layer_forward(const moe_params_t* p, const void* x, const float
                                void* out, int32_t* topk_ids_out, float* topk_w_out,
                                int32_t* counts_out, void* ws, size_t ws_bytes, void* stream);
 
-/* Same layer with HOST activations: x_host (and x_scale_host for FP8) are copied to the
+/* moe_add_rms_norm and then moe_layer_forward on its output, which stays in ws (at least
+ * moe_workspace_size_norm() bytes): the feed-forward half of a decoder layer, bit for bit as
+ * the two calls.  x, residual, residual_out, norm_w and eps as for moe_add_rms_norm (x in bf16
+ * for every dtype), the rest as for moe_layer_forward; out may not overlap x or residual. */
+moe_status_t moe_norm_layer_forward(const moe_params_t* p, const void* x, const void* residual,
+                                    const void* norm_w, float eps, void* residual_out,
+                                    const void* w_r, const float* bias, const void* w_gate,
+                                    const void* w_up, const void* w_down,
+                                    const void* w_gate_scale, const void* w_up_scale,
+                                    const void* w_down_scale, const void* ws_gate,
+                                    const void* ws_up, const void* ws_down, void* out,
+                                    int32_t* topk_ids_out, float* topk_w_out,
+                                    int32_t* counts_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Same layer with HOST activations: x_host (and x_scale_host for FP8 and INT8) are copied to the
  * device inside the call and the result is copied back to out_host, all enqueued on
  * `stream`.  Weights (and their FP8 scales) stay device pointers.  Host buffers should
  * be pinned; they must stay valid until the stream has passed this call
@@ -275,14 +343,14 @@ moe_status_t moe_layer_forward_host(const moe_params_t* p, const void* x_host,
                                     size_t ws_bytes, void* stream);
 
 /* The same layer over n_batches independent batches of T tokens, each from and to host
- * memory: batch b's x_host[b] (and x_scale_host[b] for FP8) is copied in, the layer
+ * memory: batch b's x_host[b] (and x_scale_host[b] for FP8, INT8) is copied in, the layer
  * runs, and its output is copied to out_host[b].  The copies run on two copy streams of
  * the library's own and overlap the device work of the neighbouring batches (two device
  * staging slots in ws, so batch b+1 is copied in and batch b-1 copied out while batch b
  * runs); the layer itself runs on `stream`.  The call enqueues everything and returns;
  * `stream` passes the call once every output copy has finished, and the first copy in
- * starts after the work already on `stream`.  Arrays x_host, x_scale_host (FP8 only,
- * else NULL) and out_host hold n_batches host pointers each; the same pointer may
+ * starts after the work already on `stream`.  Arrays x_host, x_scale_host (FP8 and INT8
+ * only, else NULL) and out_host hold n_batches host pointers each; the same pointer may
  * repeat.  Host buffers must be pinned for the copies to overlap and must stay valid
  * until `stream` has passed the call.  ws must hold moe_workspace_size_host() bytes.
  * Calls on one device share the copy streams.  n_batches = 0 does nothing. */
@@ -330,7 +398,8 @@ const char* moe_status_string(moe_status_t s);
 int32_t moe_abi_version(void);
 
 /* Kernel ids for tracing.  MOE_K_PERM_GATHER also covers the layer's token-order copy and
- * MOE_K_SCALE_ATOMS the e4m3 weights' scale atoms.  Where moe_layer_forward runs the
+ * MOE_K_SCALE_ATOMS the e4m3 weights' scale atoms; MOE_K_QUANT_H is the int8 experts' h to its
+ * codes, MOE_K_LINEAR the dense int8 product.  Where moe_layer_forward runs the
  * shared expert as one more group of the routed two-M-tile launches (bf16, more than 16384
  * pairs, T*K >= 256*E), its work is inside MOE_K_GATEUP / MOE_K_DOWN and the two
  * MOE_K_SHARED_* ids do not occur. */
@@ -338,7 +407,7 @@ enum {
   MOE_K_ROUTER_GEMM = 0, MOE_K_TOPK = 1, MOE_K_PERM_COUNT = 2, MOE_K_PERM_SCAN = 3,
   MOE_K_PERM_RANK = 4, MOE_K_PERM_GATHER = 5, MOE_K_GATEUP = 6, MOE_K_DOWN = 7,
   MOE_K_SHARED_GATEUP = 8, MOE_K_SHARED_DOWN = 9, MOE_K_COMBINE = 10, MOE_K_DEQUANT_X = 11,
-  MOE_K_SCALE_ATOMS = 12, MOE_K_COUNT = 13
+  MOE_K_SCALE_ATOMS = 12, MOE_K_NORM = 13, MOE_K_QUANT_H = 14, MOE_K_LINEAR = 15, MOE_K_COUNT = 16
 };
 
 /* Tracing: while enabled, every launch of a kernel whose bit (1u << id) is in

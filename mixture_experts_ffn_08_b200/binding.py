@@ -29,10 +29,13 @@ BLOCK_M = 128
 # Kernel ids for tracing (include/moe.h).
 K_ROUTER_GEMM, K_TOPK, K_PERM_COUNT, K_PERM_SCAN, K_PERM_RANK, K_PERM_GATHER = range(6)
 K_GATEUP, K_DOWN, K_SHARED_GATEUP, K_SHARED_DOWN, K_COMBINE, K_DEQUANT_X = range(6, 12)
-K_SCALE_ATOMS = 12
+K_SCALE_ATOMS, K_NORM, K_QUANT_H, K_LINEAR = range(12, 16)
 KERNEL_NAMES = ["router_gemm", "topk", "perm_count", "perm_scan", "perm_rank", "perm_gather",
                 "gateup_swiglu", "down", "shared_gateup", "shared_down", "combine", "dequant_x",
-                "scale_atoms"]
+                "scale_atoms", "norm", "quant_h", "linear"]
+
+# Output types of moe_linear_int8 (include/moe.h).
+MOE_OUT_BF16, MOE_OUT_FP16, MOE_OUT_FP32 = range(3)
 
 
 class MoEError(RuntimeError):
@@ -60,6 +63,11 @@ _PP = ctypes.POINTER(MoeParams)
 _SIGS = {
     "moe_workspace_size": (ctypes.c_size_t, [_PP]),
     "moe_workspace_size_host": (ctypes.c_size_t, [_PP]),
+    "moe_workspace_size_norm": (ctypes.c_size_t, [_PP]),
+    "moe_add_rms_norm": (ctypes.c_int, [_PP, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P]),
+    "moe_norm_layer_forward": (ctypes.c_int, [_PP, _P, _P, _P, ctypes.c_float] + [_P] * 17 + [ctypes.c_size_t, _P]),
+    "moe_linear_int8": (ctypes.c_int, [ctypes.c_int32] * 3 + [_P, ctypes.c_int64, _P, _P, ctypes.c_int64, _P, _P, _P,
+                                                             ctypes.c_int64, ctypes.c_int32, _P, _P]),
     "moe_max_padded_rows": (ctypes.c_int64, [_PP]),
     "moe_effective_block_m": (ctypes.c_int32, [_PP]),
     "moe_route": (ctypes.c_int, [_PP, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
@@ -140,6 +148,10 @@ def moe_workspace_size_host(p: MoeParams) -> int:
     return lib(require_gpu=False).moe_workspace_size_host(ctypes.byref(p))
 
 
+def moe_workspace_size_norm(p: MoeParams) -> int:
+    return lib(require_gpu=False).moe_workspace_size_norm(ctypes.byref(p))
+
+
 def moe_max_padded_rows(p: MoeParams) -> int:
     return lib(require_gpu=False).moe_max_padded_rows(ctypes.byref(p))
 
@@ -153,6 +165,17 @@ def moe_layer_launch_count(p: MoeParams) -> int:
 
 
 # ------------------------------------------------------------------ stages
+def moe_add_rms_norm(p, x, residual, norm_w, eps, residual_out, out, out_scale, stream=None) -> int:
+    return lib().moe_add_rms_norm(ctypes.byref(p), _ptr(x), _ptr(residual), _ptr(norm_w), eps,
+                                  _ptr(residual_out), _ptr(out), _ptr(out_scale), _stream(stream))
+
+
+def moe_linear_int8(M, N, K, a, lda, a_scale, w, ldw, w_scale, bias, out, ldo, out_type, device_status,
+                    stream=None) -> int:
+    return lib().moe_linear_int8(M, N, K, _ptr(a), lda, _ptr(a_scale), _ptr(w), ldw, _ptr(w_scale), _ptr(bias),
+                                 _ptr(out), ldo, out_type, _ptr(device_status), _stream(stream))
+
+
 def moe_route(p, x, x_scale, w_r, bias, topk_ids, topk_w, ws, ws_bytes, stream=None) -> int:
     return lib().moe_route(ctypes.byref(p), _ptr(x), _ptr(x_scale), _ptr(w_r), _ptr(bias),
                            _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws_bytes, _stream(stream))
@@ -211,6 +234,16 @@ def moe_layer_forward(p, x, x_scale, w_r, bias, w_gate, w_up, w_down, w_gate_sca
         ctypes.byref(p), _ptr(x), _ptr(x_scale), _ptr(w_r), _ptr(bias), _ptr(w_gate), _ptr(w_up),
         _ptr(w_down), _ptr(w_gate_scale), _ptr(w_up_scale), _ptr(w_down_scale), _ptr(ws_gate),
         _ptr(ws_up), _ptr(ws_down), _ptr(out), _ptr(topk_ids_out), _ptr(topk_w_out),
+        _ptr(counts_out), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def moe_norm_layer_forward(p, x, residual, norm_w, eps, residual_out, w_r, bias, w_gate, w_up, w_down, w_gate_scale,
+                           w_up_scale, w_down_scale, ws_gate, ws_up, ws_down, out, topk_ids_out, topk_w_out,
+                           counts_out, ws, ws_bytes, stream=None) -> int:
+    return lib().moe_norm_layer_forward(
+        ctypes.byref(p), _ptr(x), _ptr(residual), _ptr(norm_w), eps, _ptr(residual_out), _ptr(w_r), _ptr(bias),
+        _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(w_gate_scale), _ptr(w_up_scale), _ptr(w_down_scale),
+        _ptr(ws_gate), _ptr(ws_up), _ptr(ws_down), _ptr(out), _ptr(topk_ids_out), _ptr(topk_w_out),
         _ptr(counts_out), _ptr(ws), ws_bytes, _stream(stream))
 
 

@@ -171,7 +171,8 @@ struct Layout {
   size_t status, logits, xb, ids, w, counts, offsets, sched, counter, row_of_pair, pair_of_row, chunk_counts;
   size_t x_perm, x_perm_scale, h, y_perm, h_sh, y_sh, total;
   size_t x_atoms, h_atoms, wg_atoms, wu_atoms, wd_atoms;
-  size_t x_stage[2], x_scale_stage[2], out_stage[2], total_host;
+  size_t hq, hq_scale;  // int8: codes and row scales of h
+  size_t x_stage[2], x_scale_stage[2], out_stage[2], total_norm, total_host;
   long long max_rows;
 };
 
@@ -179,6 +180,10 @@ struct Layout {
 bool is_fp8(const moe_params_t* p) { return p->dtype == MOE_DTYPE_FP8_E4M3 || p->dtype == MOE_DTYPE_FP8_FP4; }
 // e2m1 expert weights whose scale atoms the caller prepared (moe_prepare_fp4_scales)
 bool is_fp4(const moe_params_t* p) { return p->dtype == MOE_DTYPE_FP8_FP4; }
+// int8 activations and weights
+bool is_i8(const moe_params_t* p) { return p->dtype == MOE_DTYPE_INT8; }
+// activations in 8 bits, with fp32 scales
+bool is_8bit(const moe_params_t* p) { return x_scales_per_row(*p) > 0; }
 
 // Bucket alignment: 128 rows (one-SM GEMM tiles) unless the caller asks for 256 (two-SM
 // cta_group::2 tiles).  Measured on B200, the pair tiles' third less SM-side traffic did
@@ -194,13 +199,14 @@ Layout layout(const moe_params_t* p) {
   const long long rows = p->masked_cap > 0 ? E * p->masked_cap : P + E * (bm - 1);
   const long long rows_t = (rows + kBlockM2 - 1) / kBlockM2 * kBlockM2;  // whole M-tile pairs
   const long long nchunks = (P + kPermChunk - 1) / kPermChunk;
-  const size_t xelem = is_fp8(p) ? 1 : 2;
+  const size_t xelem = is_8bit(p) ? 1 : 2;
+  const size_t xscales = x_scales_per_row(*p);
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o += up(bytes); return at; };
   L.max_rows = rows;
   L.status = take(256);
   L.logits = take(router_k_splits(T, p->H, p->E) * T * E * 4);  // one [T,E] slice per K-slice
-  L.xb = take(is_fp8(p) ? T * H * 2 : 0);
+  L.xb = take(is_8bit(p) ? T * H * 2 : 0);
   L.ids = take(P * 4);
   L.w = take(P * 4);
   L.counts = take(E * 4);
@@ -211,8 +217,10 @@ Layout layout(const moe_params_t* p) {
   L.pair_of_row = take(rows * 4);
   L.chunk_counts = take((nchunks > 0 ? nchunks : 1) * E * 4);
   L.x_perm = take(rows * H * xelem);
-  L.x_perm_scale = take(is_fp8(p) ? rows * (H / 128) * 4 : 0);
-  L.h = take(rows_t * I * 2);
+  L.x_perm_scale = take(rows * xscales * 4);
+  L.h = take(rows_t * I * (is_i8(p) ? 4 : 2));  // int8: fp32, until its rows' scales are known
+  L.hq = take(is_i8(p) ? rows_t * I : 0);
+  L.hq_scale = take(is_i8(p) ? rows_t * 4 : 0);
   L.y_perm = take(rows * H * 4);
   L.h_sh = take(T * static_cast<long long>(p->I_shared) * 2);
   L.y_sh = take(p->I_shared > 0 || p->fused_combine ? T * H * 4 : 0);  // also the fused-combine accumulator
@@ -228,7 +236,8 @@ Layout layout(const moe_params_t* p) {
   L.total = o;
   for (int slot = 0; slot < 2; ++slot) {  // host entry points: two device staging slots
     L.x_stage[slot] = take(T * H * xelem);
-    L.x_scale_stage[slot] = take(is_fp8(p) ? T * (H / 128) * 4 : 0);
+    L.x_scale_stage[slot] = take(T * xscales * 4);
+    if (slot == 0) L.total_norm = o;  // the normed layer keeps its input in the first slot
     L.out_stage[slot] = take(T * H * 2);
   }
   L.total_host = o;
@@ -245,7 +254,8 @@ moe_status_t validate(const moe_params_t* p) {
   if (p->T < 0 || p->H <= 0 || p->I <= 0 || p->E <= 0 || p->K <= 0) return MOE_ERR_INVALID_ARG;
   if (p->E > kMaxExperts || p->K > kMaxTopK || p->K > p->E) return MOE_ERR_INVALID_ARG;
   if (p->score_fn != MOE_SCORE_SOFTMAX && p->score_fn != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
-  if (p->dtype != MOE_DTYPE_BF16 && p->dtype != MOE_DTYPE_FP8_E4M3 && p->dtype != MOE_DTYPE_FP8_FP4)
+  if (p->dtype != MOE_DTYPE_BF16 && p->dtype != MOE_DTYPE_FP8_E4M3 && p->dtype != MOE_DTYPE_FP8_FP4 &&
+      p->dtype != MOE_DTYPE_INT8)
     return MOE_ERR_INVALID_ARG;
   if (p->n_group < 1 || p->n_group > 32 || p->E % p->n_group != 0) return MOE_ERR_INVALID_ARG;
   if (p->n_group > 1) {
@@ -257,8 +267,9 @@ moe_status_t validate(const moe_params_t* p) {
   if (p->I_shared < 0) return MOE_ERR_INVALID_ARG;
   if (p->H % 128 != 0 || p->I % 128 != 0 || p->I_shared % 128 != 0) return MOE_ERR_UNSUPPORTED;
   if (p->block_m != 0 && p->block_m != kBlockM && p->block_m != kBlockM2) return MOE_ERR_UNSUPPORTED;
-  if (is_fp8(p) && p->I_shared > 0) return MOE_ERR_UNSUPPORTED;
-  if (is_fp4(p) && p->block_m == kBlockM2) return MOE_ERR_UNSUPPORTED;
+  if (is_8bit(p) && p->I_shared > 0) return MOE_ERR_UNSUPPORTED;
+  if ((is_fp4(p) || is_i8(p)) && p->block_m == kBlockM2) return MOE_ERR_UNSUPPORTED;
+  if (is_i8(p) && (p->H > kMaxInt8K || p->I > kMaxInt8K)) return MOE_ERR_UNSUPPORTED;
   if (p->fused_combine != 0 && p->fused_combine != 1) return MOE_ERR_INVALID_ARG;
   if (p->fused_combine && (p->dtype != MOE_DTYPE_BF16 || p->block_m == kBlockM2)) return MOE_ERR_UNSUPPORTED;
   const long long rows = static_cast<long long>(p->T) * p->K + static_cast<long long>(p->E) * (kBlockM2 - 1);
@@ -271,14 +282,15 @@ moe_status_t validate(const moe_params_t* p) {
   return MOE_OK;
 }
 
+bool aligned4(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; }
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 bool aligned32(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 31u) == 0; }
 
-// Weight scales as the FFN reads them: fp32 block scales (e4m3 weights) or prepared
-// 512-byte atoms (e2m1 weights, read with 16-byte bulk copies).
+// Weight scales as the FFN reads them: fp32 block scales (e4m3 weights), fp32 channel scales
+// (int8 weights) or prepared 512-byte atoms (e2m1 weights, read with 16-byte bulk copies).
 bool weight_scales_ok(const moe_params_t* p, const void* g, const void* u, const void* d) {
-  if (!is_fp8(p)) return true;
-  if (!g || !u || !d) return false;
+  if (!is_8bit(p)) return true;
+  if (!g || !u || !d || !aligned4(g) || !aligned4(u) || !aligned4(d)) return false;
   return !is_fp4(p) || (aligned16(g) && aligned16(u) && aligned16(d));
 }
 
@@ -287,6 +299,11 @@ moe_status_t check_ws(const moe_params_t* p, const void* ws, size_t ws_bytes, bo
   const Layout L = layout(p);
   if (ws_bytes < (host ? L.total_host : L.total)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
+}
+
+moe_status_t check_ws_norm(const moe_params_t* p, const void* ws, size_t ws_bytes) {
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MOE_ERR_INVALID_ARG;
+  return ws_bytes < layout(p).total_norm ? MOE_ERR_INVALID_ARG : MOE_OK;
 }
 
 moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -308,10 +325,14 @@ moe_status_t do_route(const moe_params_t* p, const void* x, const float* x_scale
   if (is_fp8(p)) {
     MOE_CUDA(launch_dequant_x(static_cast<const uint8_t*>(x), x_scale, p->T, p->H, at<void>(ws, L.xb), st));
     xb = at<void>(ws, L.xb);
+  } else if (is_i8(p)) {
+    // the codes are exact in bf16; a token's scale is applied to its logits
+    MOE_CUDA(launch_codes_to_bf16(x, static_cast<long long>(p->T) * p->H, at<void>(ws, L.xb), st));
+    xb = at<void>(ws, L.xb);
   }
   float* logits = at<float>(ws, L.logits);
   MOE_CUDA(gemm_router(xb, w_r, p->T, p->H, p->E, logits, status, st));
-  MOE_CUDA(launch_topk(logits, *p, bias, ids, w, st, router_k_splits(p->T, p->H, p->E)));
+  MOE_CUDA(launch_topk(logits, *p, bias, ids, w, st, router_k_splits(p->T, p->H, p->E), is_i8(p) ? x_scale : nullptr));
   return MOE_OK;
 }
 
@@ -381,6 +402,24 @@ moe_status_t do_expert_ffn_fp8(const moe_params_t* p, const void* x_perm, const 
   return MOE_OK;
 }
 
+moe_status_t do_expert_ffn_i8(const moe_params_t* p, const void* x_perm, const float* x_perm_scale,
+                              const int32_t* offsets, const int32_t* counts, const void* w_gate, const void* w_up,
+                              const void* w_down, const float* gate_scale, const float* up_scale,
+                              const float* down_scale, void* y_perm, void* ws, cudaStream_t st) {
+  const Layout L = layout(p);
+  int32_t* status = at<int32_t>(ws, L.status);
+  float* h = at<float>(ws, L.h);
+  // (the kernels take the schedule from the counts, in both layouts)
+  const bool pair = static_cast<long long>(p->T) * p->K >= 256LL * p->E;
+  const I8Rows x{x_perm, x_perm_scale, L.max_rows, offsets, counts, p->E, p->masked_cap};
+  const I8Rows hq{at<void>(ws, L.hq), at<float>(ws, L.hq_scale), L.max_rows, offsets, counts, p->E, p->masked_cap};
+  MOE_CUDA(gemm_i8_gateup_swiglu(x, w_gate, w_up, gate_scale, up_scale, p->I, p->H, h, status, pair, st));
+  MOE_CUDA(launch_quant_rows(h, L.max_rows, offsets, counts, p->E, p->masked_cap, p->I, at<void>(ws, L.hq),
+                             at<float>(ws, L.hq_scale), st));
+  MOE_CUDA(gemm_i8_down(hq, w_down, down_scale, p->H, p->I, y_perm, status, pair, st));
+  return MOE_OK;
+}
+
 // Gate/up with SwiGLU of the routed experts.  When the average expert holds at least two
 // 128-row M-tiles (T*K >= 256*E) the two-tile kernel runs: one staged weight tile feeds the
 // MMAs of two M-tiles (measured on B200: DeepSeek-V3 prefill gate/up 3.92 against 4.12 ms,
@@ -411,7 +450,7 @@ moe_status_t do_gateup(const moe_params_t* p, const void* x_perm, const int32_t*
 // An output beyond fp16's range (|y| > 65504) sets MOE_DEV_RANGE.  The stage entry points
 // (moe_expert_ffn, moe_combine) keep fp32 y_perm.
 bool layer_y16(const moe_params_t* p, const int32_t* counts) {
-  return two_tile_items(p, counts) && p->H % 256 == 0 && !is_fp8(p);
+  return two_tile_items(p, counts) && p->H % 256 == 0 && !is_8bit(p);
 }
 
 // The shared expert of a bf16 layer on one stream (prefill sizes: its T rows hold at least
@@ -557,6 +596,10 @@ moe_status_t do_layer_after_fork(const moe_params_t* p, const void* x, const flo
   if (is_fp8(p)) {
     MOE_TRY(do_expert_ffn_fp8(p, at<void>(ws, L.x_perm), at<float>(ws, L.x_perm_scale), offsets, counts,
                               w_gate, w_up, w_down, wgs, wus, wds, y_perm, ws, st, /*x_atoms_ready=*/true));
+  } else if (is_i8(p)) {
+    MOE_TRY(do_expert_ffn_i8(p, at<void>(ws, L.x_perm), at<float>(ws, L.x_perm_scale), offsets, counts, w_gate, w_up,
+                             w_down, static_cast<const float*>(wgs), static_cast<const float*>(wus),
+                             static_cast<const float*>(wds), y_perm, ws, st));
   } else if (merged) {
     // the shared expert as the extra group of the routed two-tile launches, y_sh in fp16
     const DualExtra gu{x, p->T, wsg, wsu, p->I_shared, p->H, at<void>(ws, L.h_sh)};
@@ -595,12 +638,22 @@ moe_status_t check_layer_args(const moe_params_t* p, const void* x, const float*
   if (!aligned16(x) || !aligned16(w_r) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(w_down) ||
       !aligned16(out))
     return MOE_ERR_INVALID_ARG;
-  if (is_fp8(p) && !x_scale) return MOE_ERR_INVALID_ARG;
+  if (is_8bit(p) && (!x_scale || !aligned4(x_scale))) return MOE_ERR_INVALID_ARG;
   if (is_fp4(p) && !(aligned32(w_gate) && aligned32(w_up) && aligned32(w_down))) return MOE_ERR_INVALID_ARG;
   if (p->I_shared > 0) {
     if (!wsg || !wsu || !wsd) return MOE_ERR_INVALID_ARG;
     if (!aligned16(wsg) || !aligned16(wsu) || !aligned16(wsd)) return MOE_ERR_INVALID_ARG;
   }
+  return MOE_OK;
+}
+
+moe_status_t check_norm_args(const moe_params_t* p, const void* x, const void* residual, const void* norm_w, float eps,
+                             const void* residual_out) {
+  if (!(eps >= 1.1754943508222875e-38f) || eps > 3.0e38f) return MOE_ERR_INVALID_ARG;  // a positive normal number
+  if (p->T == 0) return MOE_OK;
+  if (!x || !norm_w || (residual_out && !residual)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(norm_w) || !aligned16(residual_out))
+    return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
@@ -614,6 +667,11 @@ extern "C" {
 size_t moe_workspace_size(const moe_params_t* p) {
   if (validate(p) != MOE_OK) return 0;
   return layout(p).total;
+}
+
+size_t moe_workspace_size_norm(const moe_params_t* p) {
+  if (validate(p) != MOE_OK) return 0;
+  return layout(p).total_norm;
 }
 
 size_t moe_workspace_size_host(const moe_params_t* p) {
@@ -638,7 +696,7 @@ moe_status_t moe_route(const moe_params_t* p, const void* x, const float* x_scal
   MOE_TRY(check_ws(p, ws, ws_bytes, false));
   if (p->T == 0) return MOE_OK;  // empty batch: nothing to read or write
   if (!x || !w_r || !topk_ids || !topk_w || !aligned16(x) || !aligned16(w_r)) return MOE_ERR_INVALID_ARG;
-  if (is_fp8(p) && !x_scale) return MOE_ERR_INVALID_ARG;
+  if (is_8bit(p) && (!x_scale || !aligned4(x_scale))) return MOE_ERR_INVALID_ARG;
   return do_route(p, x, x_scale, w_r, bias, topk_ids, topk_w, ws, static_cast<cudaStream_t>(stream));
 }
 
@@ -667,7 +725,8 @@ moe_status_t moe_permute(const moe_params_t* p, const int32_t* topk_ids, const v
   if ((!empty && (!topk_ids || !x || !row_of_pair)) || !counts || !offsets_padded || !pair_of_row || !x_perm)
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(x_perm)) return MOE_ERR_INVALID_ARG;
-  if (is_fp8(p) && ((!empty && !x_scale) || !x_perm_scale)) return MOE_ERR_INVALID_ARG;
+  if (is_8bit(p) && ((!empty && !x_scale) || !x_perm_scale || !aligned4(x_scale) || !aligned4(x_perm_scale)))
+    return MOE_ERR_INVALID_ARG;
   return do_permute(p, topk_ids, x, x_scale, counts, offsets_padded, row_of_pair, pair_of_row, x_perm,
                     x_perm_scale, ws, static_cast<cudaStream_t>(stream));
 }
@@ -684,9 +743,13 @@ moe_status_t moe_expert_ffn(const moe_params_t* p, const void* x_perm, const flo
   if (p->masked_cap > 0 ? !counts : !offsets_padded) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x_perm) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(w_down) || !aligned16(y_perm))
     return MOE_ERR_INVALID_ARG;
-  if (is_fp8(p) && !x_perm_scale) return MOE_ERR_INVALID_ARG;
+  if (is_8bit(p) && (!x_perm_scale || !aligned4(x_perm_scale))) return MOE_ERR_INVALID_ARG;
   if (!weight_scales_ok(p, w_gate_scale, w_up_scale, w_down_scale)) return MOE_ERR_INVALID_ARG;
   if (is_fp4(p) && !(aligned32(w_gate) && aligned32(w_up) && aligned32(w_down))) return MOE_ERR_INVALID_ARG;
+  if (is_i8(p))
+    return do_expert_ffn_i8(p, x_perm, x_perm_scale, offsets_padded, counts, w_gate, w_up, w_down,
+                            static_cast<const float*>(w_gate_scale), static_cast<const float*>(w_up_scale),
+                            static_cast<const float*>(w_down_scale), y_perm, ws, static_cast<cudaStream_t>(stream));
   if (offsets_padded == nullptr) {  // masked layout: expert e's rows start at e*cap
     const Layout L = layout(p);
     int32_t* offs = at<int32_t>(ws, L.offsets);
@@ -706,7 +769,7 @@ moe_status_t moe_shared_expert_ffn(const moe_params_t* p, const void* x, const v
                                    size_t ws_bytes, void* stream) {
   MOE_TRY(validate(p));
   MOE_TRY(check_ws(p, ws, ws_bytes, false));
-  if (p->I_shared <= 0 || is_fp8(p)) return MOE_ERR_UNSUPPORTED;
+  if (p->I_shared <= 0 || is_8bit(p)) return MOE_ERR_UNSUPPORTED;
   if (p->T == 0) return MOE_OK;
   if (!x || !ws_gate || !ws_up || !ws_down || !y_shared) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(ws_gate) || !aligned16(ws_up) || !aligned16(ws_down) || !aligned16(y_shared))
@@ -743,6 +806,54 @@ moe_status_t moe_layer_forward(const moe_params_t* p, const void* x, const float
                   topk_w_out, counts_out, ws, static_cast<cudaStream_t>(stream));
 }
 
+moe_status_t moe_add_rms_norm(const moe_params_t* p, const void* x, const void* residual, const void* norm_w, float eps,
+                              void* residual_out, void* out, float* out_scale, void* stream) {
+  MOE_TRY(validate(p));
+  MOE_TRY(check_norm_args(p, x, residual, norm_w, eps, residual_out));
+  if (p->T == 0) return MOE_OK;
+  if (!out || !aligned16(out) || (is_8bit(p) && (!out_scale || !aligned4(out_scale)))) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_add_rms_norm(*p, x, residual, norm_w, eps, residual_out, out, out_scale,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_norm_layer_forward(const moe_params_t* p, const void* x, const void* residual, const void* norm_w,
+                                    float eps, void* residual_out, const void* w_r, const float* bias,
+                                    const void* w_gate, const void* w_up, const void* w_down,
+                                    const void* w_gate_scale, const void* w_up_scale, const void* w_down_scale,
+                                    const void* ws_gate, const void* ws_up, const void* ws_down, void* out,
+                                    int32_t* topk_ids_out, float* topk_w_out, int32_t* counts_out, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  MOE_TRY(validate(p));
+  MOE_TRY(check_ws_norm(p, ws, ws_bytes));
+  MOE_TRY(check_norm_args(p, x, residual, norm_w, eps, residual_out));
+  const Layout L = layout(p);
+  void* y = at<void>(ws, L.x_stage[0]);
+  float* ys = is_8bit(p) ? at<float>(ws, L.x_scale_stage[0]) : nullptr;
+  if (p->T > 0) {  // every check before the first launch
+    MOE_TRY(check_layer_args(p, y, ys, w_r, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, out));
+    if (!weight_scales_ok(p, w_gate_scale, w_up_scale, w_down_scale)) return MOE_ERR_INVALID_ARG;
+    MOE_CUDA(launch_add_rms_norm(*p, x, residual, norm_w, eps, residual_out, y, ys, static_cast<cudaStream_t>(stream)));
+  }
+  return moe_layer_forward(p, y, ys, w_r, bias, w_gate, w_up, w_down, w_gate_scale, w_up_scale, w_down_scale, ws_gate,
+                           ws_up, ws_down, out, topk_ids_out, topk_w_out, counts_out, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_linear_int8(int32_t M, int32_t N, int32_t K, const void* a, int64_t lda, const float* a_scale,
+                             const void* w, int64_t ldw, const float* w_scale, const float* bias, void* out,
+                             int64_t ldo, int32_t out_type, int32_t* device_status, void* stream) {
+  if (M < 0 || N <= 0 || K <= 0 || lda < K || ldw < K || ldo < N) return MOE_ERR_INVALID_ARG;
+  if (out_type != MOE_OUT_BF16 && out_type != MOE_OUT_FP16 && out_type != MOE_OUT_FP32) return MOE_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K > kMaxInt8K || lda % 16 != 0 || ldw % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  const long long tiles = (M + 127LL) / 128 * ((N + 31LL) / 32);
+  if (tiles > INT32_MAX || lda >= (1LL << 40) || ldw >= (1LL << 40)) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!a || !a_scale || !w || !w_scale || !out || !aligned16(a) || !aligned16(w)) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(a_scale) || !aligned4(w_scale) || !aligned4(bias) || !aligned4(device_status)) return MOE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(out) & (out_type == MOE_OUT_FP32 ? 3u : 1u)) != 0) return MOE_ERR_INVALID_ARG;
+  return cuda_status(gemm_i8_linear(M, N, K, a, lda, a_scale, w, ldw, w_scale, bias, out_type, out, ldo, device_status,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
 moe_status_t moe_layer_forward_host(const moe_params_t* p, const void* x_host, const float* x_scale_host,
                                     const void* w_r, const float* bias, const void* w_gate, const void* w_up,
                                     const void* w_down, const void* w_gate_scale, const void* w_up_scale,
@@ -753,18 +864,18 @@ moe_status_t moe_layer_forward_host(const moe_params_t* p, const void* x_host, c
   MOE_TRY(check_ws(p, ws, ws_bytes, true));
   if (p->T == 0) return MOE_OK;
   if (!x_host || !out_host) return MOE_ERR_INVALID_ARG;
-  if (is_fp8(p) && !x_scale_host) return MOE_ERR_INVALID_ARG;
+  if (is_8bit(p) && !x_scale_host) return MOE_ERR_INVALID_ARG;
   if (!weight_scales_ok(p, w_gate_scale, w_up_scale, w_down_scale)) return MOE_ERR_INVALID_ARG;
   const Layout L = layout(p);
   void* x_dev = at<void>(ws, L.x_stage[0]);
-  float* xs_dev = is_fp8(p) ? at<float>(ws, L.x_scale_stage[0]) : nullptr;
+  float* xs_dev = is_8bit(p) ? at<float>(ws, L.x_scale_stage[0]) : nullptr;
   void* out_dev = at<void>(ws, L.out_stage[0]);
   MOE_TRY(check_layer_args(p, x_dev, xs_dev, w_r, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, out_dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const size_t xbytes = static_cast<size_t>(p->T) * p->H * (is_fp8(p) ? 1 : 2);
+  const size_t xbytes = static_cast<size_t>(p->T) * p->H * (is_8bit(p) ? 1 : 2);
   MOE_CUDA(cudaMemcpyAsync(x_dev, x_host, xbytes, cudaMemcpyHostToDevice, st));
-  if (is_fp8(p))
-    MOE_CUDA(cudaMemcpyAsync(xs_dev, x_scale_host, static_cast<size_t>(p->T) * (p->H / 128) * sizeof(float),
+  if (is_8bit(p))
+    MOE_CUDA(cudaMemcpyAsync(xs_dev, x_scale_host, static_cast<size_t>(p->T) * x_scales_per_row(*p) * sizeof(float),
                              cudaMemcpyHostToDevice, st));
   MOE_TRY(do_layer(p, x_dev, xs_dev, w_r, bias, w_gate, w_up, w_down, w_gate_scale, w_up_scale, w_down_scale,
                    ws_gate, ws_up, ws_down, out_dev, nullptr, nullptr, nullptr, ws, st));
@@ -783,21 +894,21 @@ moe_status_t moe_layer_forward_host_batches(const moe_params_t* p, int32_t n_bat
   MOE_TRY(check_ws(p, ws, ws_bytes, true));
   if (n_batches < 0) return MOE_ERR_INVALID_ARG;
   if (n_batches == 0 || p->T == 0) return MOE_OK;
-  if (!x_host || !out_host || (is_fp8(p) && !x_scale_host)) return MOE_ERR_INVALID_ARG;
+  if (!x_host || !out_host || (is_8bit(p) && !x_scale_host)) return MOE_ERR_INVALID_ARG;
   for (int32_t b = 0; b < n_batches; ++b)
-    if (!x_host[b] || !out_host[b] || (is_fp8(p) && !x_scale_host[b])) return MOE_ERR_INVALID_ARG;
+    if (!x_host[b] || !out_host[b] || (is_8bit(p) && !x_scale_host[b])) return MOE_ERR_INVALID_ARG;
   if (!weight_scales_ok(p, w_gate_scale, w_up_scale, w_down_scale)) return MOE_ERR_INVALID_ARG;
   const Layout L = layout(p);
   for (int slot = 0; slot < 2; ++slot)
     MOE_TRY(check_layer_args(p, at<void>(ws, L.x_stage[slot]),
-                             is_fp8(p) ? at<float>(ws, L.x_scale_stage[slot]) : nullptr, w_r, w_gate, w_up, w_down,
+                             is_8bit(p) ? at<float>(ws, L.x_scale_stage[slot]) : nullptr, w_r, w_gate, w_up, w_down,
                              ws_gate, ws_up, ws_down, at<void>(ws, L.out_stage[slot])));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lock(g_copy_mu);
   const Copies* c = copies_for_current_device();
   if (c == nullptr) return MOE_ERR_CUDA;
-  const size_t xbytes = static_cast<size_t>(p->T) * p->H * (is_fp8(p) ? 1 : 2);
-  const size_t sbytes = static_cast<size_t>(p->T) * (p->H / 128) * sizeof(float);
+  const size_t xbytes = static_cast<size_t>(p->T) * p->H * (is_8bit(p) ? 1 : 2);
+  const size_t sbytes = static_cast<size_t>(p->T) * x_scales_per_row(*p) * sizeof(float);
   const size_t obytes = static_cast<size_t>(p->T) * p->H * 2;
   // the first copy in comes after the work already on the caller's stream
   MOE_CUDA(cudaEventRecord(c->fork, st));
@@ -807,12 +918,12 @@ moe_status_t moe_layer_forward_host_batches(const moe_params_t* p, int32_t n_bat
   for (int32_t b = 0; b < n_batches && status == MOE_OK; ++b) {
     const int slot = b & 1;
     void* x_dev = at<void>(ws, L.x_stage[slot]);
-    float* xs_dev = is_fp8(p) ? at<float>(ws, L.x_scale_stage[slot]) : nullptr;
+    float* xs_dev = is_8bit(p) ? at<float>(ws, L.x_scale_stage[slot]) : nullptr;
     void* out_dev = at<void>(ws, L.out_stage[slot]);
     // in: the slot's activations were read by the layer of batch b-2 (done[slot])
     if (b >= 2) MOE_CUDA(cudaStreamWaitEvent(c->in, c->done[slot], 0));
     MOE_CUDA(cudaMemcpyAsync(x_dev, x_host[b], xbytes, cudaMemcpyHostToDevice, c->in));
-    if (is_fp8(p)) MOE_CUDA(cudaMemcpyAsync(xs_dev, x_scale_host[b], sbytes, cudaMemcpyHostToDevice, c->in));
+    if (is_8bit(p)) MOE_CUDA(cudaMemcpyAsync(xs_dev, x_scale_host[b], sbytes, cudaMemcpyHostToDevice, c->in));
     MOE_CUDA(cudaEventRecord(c->landed[slot], c->in));
     // the layer: after its activations landed and the slot's previous output left
     MOE_CUDA(cudaStreamWaitEvent(st, c->landed[slot], 0));
@@ -915,12 +1026,13 @@ int32_t moe_layer_launch_count(const moe_params_t* p) {
   int n = 2;                                 // router GEMM, top-k
   if (is_fp8(p)) n += is_fp4(p) ? 1 : 4;     // dequantise x for the router (and the scale atoms
                                              // of the three e4m3 weights; x's come with the copy)
+  if (is_i8(p)) n += 2;                      // x's codes in bf16 for the router, h's codes
   const long long P = static_cast<long long>(p->T) * p->K;
   n += P <= kSmallPairs ? 2 : 4;             // count, scan, rank (one kernel for few pairs), gather
   n += 2;                                    // gate/up, down
   if (p->I_shared > 0 && !shared_merged(p)) n += 2;  // shared gate/up, down (unless in the routed ones)
   n += 1;                                    // combine
-  if (p->masked_cap > 0) n += 1;             // compact GEMM schedule of the masked layout
+  if (p->masked_cap > 0 && !is_i8(p)) n += 1;  // compact GEMM schedule of the masked layout
   return n;
 }
 

@@ -1,0 +1,258 @@
+// Host side of the int8 products (tc_gemm_i8.cuh): tensor maps, the choice of tile, launches;
+// and the re-quantisation of the experts' intermediate h.
+#include <cudaTypedefs.h>
+#include <math_constants.h>
+
+#include "internal.h"
+#include "tc_gemm_i8.cuh"
+
+namespace moe {
+
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn_i8() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr) : nullptr;
+  }();
+  return fn;
+}
+
+// 8-bit matrix [rows, cols] with row stride ld bytes: boxes of 128 columns (one 128-byte swizzle
+// row) x box_rows rows; what lies outside the matrix reads as zero and adds nothing.
+bool make_tmap_i8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+  auto fn = encode_fn_i8();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+
+// A [a_rows, K] (row stride lda), B [b_rows, K] (row stride ldb; b1: SWIGLU's up weights).
+template <class Cfg>
+cudaError_t launch_i8(const void* A, int64_t a_rows, int64_t lda, const void* b0, const void* b1, int64_t b_rows,
+                      int64_t ldb, const I8Params& p, long long max_items, int kid, cudaStream_t st) {
+  constexpr uint32_t b_box = Cfg::SWIGLU ? 128 : Cfg::B_ROWS;
+  CUtensorMap ta, ta32, tb0, tb1;
+  if (!make_tmap_i8(&ta, A, a_rows, p.K, lda, 128) || !make_tmap_i8(&ta32, A, a_rows, p.K, lda, kI8SmallRows) ||
+      !make_tmap_i8(&tb0, b0, b_rows, p.K, ldb, b_box) || !make_tmap_i8(&tb1, b1, b_rows, p.K, ldb, b_box))
+    return cudaErrorInvalidValue;
+  auto kern = tc_gemm_i8_kernel<Cfg>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+  if (err != cudaSuccess) return err;
+  const long long most = num_sms() / Cfg::CG;
+  const long long n = max_items < most ? (max_items > 0 ? max_items : 1) : most;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(Cfg::CG * n), 1, 1);
+  cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  if (pdl_enabled()) {
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+  }
+  if (Cfg::CG > 1) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = Cfg::CG;
+    attr[na].val.clusterDim.y = 1;
+    attr[na].val.clusterDim.z = 1;
+    ++na;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = na;
+  trace_before(kid, st);
+  err = cudaLaunchKernelEx(&cfg, kern, ta, ta32, tb0, tb1, p);
+  trace_after(kid, st);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ h -> int8
+// q = rint(h / s), s = max|h| / 127 over the row (1 where the row is zero), as int8 codes and one
+// fp32 scale per row.  A row with a NaN or an infinity gets codes 0 and scale NaN, so that its
+// outputs are NaN.  Only the groups' real rows are read and written.  A warp per row, in two
+// passes: the row's largest value, then the codes.
+constexpr int kQuantWarps = 8;
+
+MOE_DEVINL uint32_t quant4(float4 v, float f) {
+  return (static_cast<uint32_t>(__float2int_rn(v.x * f)) & 0xffu) |
+         (static_cast<uint32_t>(__float2int_rn(v.y * f)) & 0xffu) << 8 |
+         (static_cast<uint32_t>(__float2int_rn(v.z * f)) & 0xffu) << 16 |
+         (static_cast<uint32_t>(__float2int_rn(v.w * f)) & 0xffu) << 24;
+}
+
+MOE_DEVINL uint32_t absmax4(uint32_t m, float4 v) {
+  m = max(m, __float_as_uint(v.x) & 0x7fffffffu);
+  m = max(m, __float_as_uint(v.y) & 0x7fffffffu);
+  m = max(m, __float_as_uint(v.z) & 0x7fffffffu);
+  return max(m, __float_as_uint(v.w) & 0x7fffffffu);
+}
+
+__global__ void __launch_bounds__(32 * kQuantWarps) quant_rows_kernel(
+    const float* __restrict__ h, const int32_t* __restrict__ offsets, const int32_t* __restrict__ counts, int E,
+    int cap, int cols, int8_t* __restrict__ codes, float* __restrict__ scale) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int n4 = cols / 4;
+  const long long rows = cap > 0 ? static_cast<long long>(E) * cap : __ldg(offsets + E);
+  const long long warps = static_cast<long long>(gridDim.x) * kQuantWarps;
+  for (long long r = static_cast<long long>(blockIdx.x) * kQuantWarps + (threadIdx.x >> 5); r < rows; r += warps) {
+    if (counts != nullptr) {
+      int e;
+      long long first;
+      if (cap > 0) {
+        e = static_cast<int>(r / cap);
+        first = static_cast<long long>(e) * cap;
+      } else {
+        int lo = 0, hi = E - 1;  // smallest e with offsets[e+1] > r
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (__ldg(offsets + mid + 1) > r) hi = mid; else lo = mid + 1;
+        }
+        e = lo;
+        first = __ldg(offsets + e);
+      }
+      if (r - first >= __ldg(counts + e)) continue;
+    }
+    const float4* src = reinterpret_cast<const float4*>(h + r * cols);
+    uint32_t m = 0;
+    for (int v = lane; v < n4; v += 32) m = absmax4(m, src[v]);
+    m = __reduce_max_sync(0xffffffffu, m);
+    const float amax = __uint_as_float(m);
+    const bool bad = m >= 0x7f800000u;
+    const float s = bad ? CUDART_NAN_F : (m == 0 ? 1.f : fmaxf(amax / 127.f, 1.1754943508222875e-38f));
+    const float f = bad ? 0.f : 1.f / s;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(codes + r * cols);
+    for (int v = lane; v < n4; v += 32) dst[v] = bad ? 0u : quant4(src[v], f);
+    if (lane == 0) scale[r] = s;
+  }
+}
+
+// int8 codes as bf16 (exact), for the router's product.
+__global__ void __launch_bounds__(256) codes_to_bf16_kernel(const uint2* __restrict__ q, long long n8,
+                                                            uint4* __restrict__ out) {
+  pdl_launch_dependents();
+  pdl_wait();
+  for (long long v = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; v < n8;
+       v += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const uint2 c = __ldg(q + v);
+    const uint32_t w[2] = {c.x, c.y};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t half = w[i >> 1] >> (16 * (i & 1));
+      o[i] = pack_bf16x2(static_cast<float>(static_cast<int8_t>(half & 0xffu)),
+                         static_cast<float>(static_cast<int8_t>((half >> 8) & 0xffu)));
+    }
+    out[v] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_codes_to_bf16(const void* q, long long n, void* x_bf16, cudaStream_t st) {
+  const long long n8 = n / 8, want = cdiv(n8, 256);
+  const int grid = static_cast<int>(want < num_sms() * 8LL ? want : num_sms() * 8LL);
+  trace_before(MOE_K_DEQUANT_X, st);
+  const cudaError_t err = launch_k(codes_to_bf16_kernel, grid, 256, 0, st, static_cast<const uint2*>(q), n8,
+                                   static_cast<uint4*>(x_bf16));
+  trace_after(MOE_K_DEQUANT_X, st);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+cudaError_t launch_quant_rows(const float* h, long long max_rows, const int32_t* offsets, const int32_t* counts, int E,
+                              int cap, int cols, void* codes, float* scale, cudaStream_t st) {
+  const long long want = cdiv(max_rows, kQuantWarps);
+  const int grid = static_cast<int>(want < num_sms() * 8LL ? (want > 0 ? want : 1) : num_sms() * 8LL);
+  trace_before(MOE_K_QUANT_H, st);
+  const cudaError_t err = launch_k(quant_rows_kernel, grid, 32 * kQuantWarps, 0, st, h, offsets, counts, E, cap, cols,
+                                   static_cast<int8_t*>(codes), scale);
+  trace_after(MOE_K_QUANT_H, st);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+cudaError_t gemm_i8_gateup_swiglu(const I8Rows& a, const void* w_gate, const void* w_up, const float* gate_scale,
+                                  const float* up_scale, int N, int K, float* h, int32_t* status, bool pair,
+                                  cudaStream_t st) {
+  I8Params p{};
+  p.offsets = a.offsets;
+  p.counts = a.counts;
+  p.G = a.G;
+  p.masked_cap = a.masked_cap;
+  p.K = K;
+  p.N = N;
+  p.a_scale = a.scale;
+  p.w_scale = gate_scale;
+  p.w_scale_up = up_scale;
+  p.out = h;
+  p.ldo = N;
+  p.status = status;
+  const int64_t b_rows = static_cast<int64_t>(a.G) * N;
+  const long long items = cdiv(a.rows, 128) * cdiv(N, 128);
+  if (pair)
+    return launch_i8<I8Cfg<2, 256, true, 6>>(a.codes, a.rows, K, w_gate, w_up, b_rows, K, p, items, MOE_K_GATEUP, st);
+  return launch_i8<I8Cfg<1, 256, true, 4>>(a.codes, a.rows, K, w_gate, w_up, b_rows, K, p, items, MOE_K_GATEUP, st);
+}
+
+cudaError_t gemm_i8_down(const I8Rows& a, const void* w, const float* w_scale, int N, int K, void* y, int32_t* status,
+                         bool pair, cudaStream_t st) {
+  I8Params p{};
+  p.offsets = a.offsets;
+  p.counts = a.counts;
+  p.G = a.G;
+  p.masked_cap = a.masked_cap;
+  p.K = K;
+  p.N = N;
+  p.a_scale = a.scale;
+  p.w_scale = w_scale;
+  p.out = y;
+  p.out_type = MOE_OUT_BF16;
+  p.ldo = N;
+  p.status = status;
+  const int64_t b_rows = static_cast<int64_t>(a.G) * N;
+  const long long items = cdiv(a.rows, 128) * cdiv(N, 256);
+  if (pair)
+    return launch_i8<I8Cfg<2, 256, false, 6>>(a.codes, a.rows, K, w, w, b_rows, K, p, items, MOE_K_DOWN, st);
+  return launch_i8<I8Cfg<1, 256, false, 4>>(a.codes, a.rows, K, w, w, b_rows, K, p, items, MOE_K_DOWN, st);
+}
+
+cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, const float* a_scale, const void* w,
+                           int64_t ldw, const float* w_scale, const float* bias, int out_type, void* out, int64_t ldo,
+                           int32_t* status, cudaStream_t st) {
+  I8Params p{};
+  p.G = 1;
+  p.dense_rows = M;
+  p.K = K;
+  p.N = N;
+  p.a_scale = a_scale;
+  p.w_scale = w_scale;
+  p.bias = bias;
+  p.out = out;
+  p.out_type = out_type;
+  p.ldo = ldo;
+  p.status = status;
+  const long long sms = num_sms();
+  // pair tiles where they fill the SMs, else the widest one-SM tile that does
+  if (cdiv(M, 256) * cdiv(N, 256) >= sms / 2)
+    return launch_i8<I8Cfg<2, 256, false, 6>>(a, M, lda, w, w, N, ldw, p, cdiv(M, 256) * cdiv(N, 256), MOE_K_LINEAR, st);
+  const long long mt = cdiv(M, 128);
+  if (mt * cdiv(N, 128) >= sms)
+    return launch_i8<I8Cfg<1, 128, false, 6>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 128), MOE_K_LINEAR, st);
+  if (mt * cdiv(N, 64) >= sms)
+    return launch_i8<I8Cfg<1, 64, false, 8>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 64), MOE_K_LINEAR, st);
+  return launch_i8<I8Cfg<1, 32, false, 9>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 32), MOE_K_LINEAR, st);
+}
+
+}  // namespace moe

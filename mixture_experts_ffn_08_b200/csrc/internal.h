@@ -14,6 +14,7 @@ constexpr int kBlockM2 = 256;   // bucket alignment for the two-SM (cta_group::2
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
 constexpr int kPermChunk = 256;  // pairs per chunk of the stable bucket ranking
+constexpr int kMaxInt8K = 131071;  // longest int8 sum that cannot pass 2^31: K * 128 * 128
 constexpr int kSmallPairs = 2048;  // up to this many pairs one block counts, scans and ranks
 
 // Programmatic dependent launch of the layer's kernels (api.cu): on unless the
@@ -61,12 +62,22 @@ inline bool act_e4m3(const moe_params_t& p) {
   return p.dtype == MOE_DTYPE_FP8_E4M3 || p.dtype == MOE_DTYPE_FP8_FP4;
 }
 
+// Activations (x, h) are int8 with one fp32 scale per row.
+inline bool act_i8(const moe_params_t& p) { return p.dtype == MOE_DTYPE_INT8; }
+// fp32 scales of one row of x: per 128 channels (e4m3), one (int8), none (bf16).
+inline int x_scales_per_row(const moe_params_t& p) { return act_e4m3(p) ? p.H / 128 : (act_i8(p) ? 1 : 0); }
+
+// ---------------------------------------------------------------- norm (norm.cu)
+cudaError_t launch_add_rms_norm(const moe_params_t& p, const void* x, const void* residual, const void* w, float eps,
+                                void* residual_out, void* out, float* scale, cudaStream_t st);
+
 // ---------------------------------------------------------------- routing (kernels.cu)
 cudaError_t launch_dequant_x(const uint8_t* xq, const float* xs, int T, int H, void* x_bf16,
                              cudaStream_t st);
-// logits: n_part slices of [T, E] fp32 partial sums, summed in slice order.
+// logits: n_part slices of [T, E] fp32 partial sums, summed in slice order; row_scale [T]
+// (or nullptr): factor of a token's logits.
 cudaError_t launch_topk(const float* logits, const moe_params_t& p, const float* bias,
-                        int32_t* ids, float* w, cudaStream_t st, int n_part = 1);
+                        int32_t* ids, float* w, cudaStream_t st, int n_part = 1, const float* row_scale = nullptr);
 
 // b_e += gamma * sign(mean load - load_e) (aux-free balancing bias).
 cudaError_t launch_bias_update(const int32_t* counts, int E, float gamma, float* bias, cudaStream_t st);
@@ -92,7 +103,7 @@ cudaError_t launch_permute(const moe_params_t& p, int block_m, const int32_t* id
                            cudaStream_t st, bool fill_pad = true, uint8_t* x_atoms = nullptr);
 
 // ---------------------------------------------------------------- combine (kernels.cu)
-// y_perm is fp32 for bf16 workloads and bf16 for FP8 workloads (p.dtype).
+// y_perm is fp32 for bf16 workloads and bf16 for the 8-bit ones (p.dtype).
 // y_shared: [T,H] fp32, or fp16 when ysh_f16.
 cudaError_t launch_combine(const moe_params_t& p, const void* y_perm, const int32_t* row_of_pair,
                            const float* w, const void* y_shared, void* out, cudaStream_t st, bool y_f16 = false,
@@ -169,6 +180,35 @@ cudaError_t gemm_down_fp8(const void* A, const uint8_t* a_atoms, int64_t a_rows,
 // atoms come from launch_fp4_scale_atoms.
 // e2m1 weight scale words [rows, K/128] (4 UE8M0 bytes each) -> atoms [rows/128][K/128][512].
 cudaError_t launch_fp4_scale_atoms(const uint32_t* words, long long rows, int K, uint8_t* atoms, cudaStream_t st);
+
+// ---------------------------------------------------------------- int8 GEMMs (gemm_i8.cu)
+// n int8 codes as bf16, exactly (n a multiple of 8).
+cudaError_t launch_codes_to_bf16(const void* q, long long n, void* x_bf16, cudaStream_t st);
+// Bucketed int8 rows: the real rows of group g are the first counts[g] (nullptr: all) of those
+// from offsets[g] on, or from g * masked_cap on.
+struct I8Rows {
+  const void* codes;       // [rows, K]
+  const float* scale;      // [rows]
+  int64_t rows;
+  const int32_t* offsets;
+  const int32_t* counts;
+  int G;
+  int masked_cap;
+};
+// h [rows, N] fp32 = SiLU(A Wg^T) * (A Wu^T) on the real rows.  pair: tiles of two CTAs.
+cudaError_t gemm_i8_gateup_swiglu(const I8Rows& a, const void* w_gate, const void* w_up, const float* gate_scale,
+                                  const float* up_scale, int N, int K, float* h, int32_t* status, bool pair,
+                                  cudaStream_t st);
+// h's real rows as int8 codes with one scale per row.
+cudaError_t launch_quant_rows(const float* h, long long max_rows, const int32_t* offsets, const int32_t* counts, int E,
+                              int cap, int cols, void* codes, float* scale, cudaStream_t st);
+// y [rows, N] bf16 = A W^T on the real rows.
+cudaError_t gemm_i8_down(const I8Rows& a, const void* w, const float* w_scale, int N, int K, void* y, int32_t* status,
+                         bool pair, cudaStream_t st);
+// out [M, N] (row stride ldo) = A W^T + bias.
+cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, const float* a_scale, const void* w,
+                           int64_t ldw, const float* w_scale, const float* bias, int out_type, void* out, int64_t ldo,
+                           int32_t* status, cudaStream_t st);
 
 // ---------------------------------------------------------------- two-SM GEMMs (gemm_2cta.cu)
 cudaError_t gemm_pair_gateup_swiglu(const void* A, int64_t a_rows, const int32_t* offsets, const int32_t* counts,

@@ -100,7 +100,7 @@ template <int EPL>
 __global__ void __launch_bounds__(128) topk_kernel(
     const float* __restrict__ logits, int n_part, int T, int E, int K, int n_group, int topk_group,
     int group_topn, int score_fn, int renorm, float scale, const float* __restrict__ bias,
-    int32_t* __restrict__ ids, float* __restrict__ wout) {
+    const float* __restrict__ row_scale, int32_t* __restrict__ ids, float* __restrict__ wout) {
   pdl_launch_dependents();
   pdl_wait();
   const int token = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -140,6 +140,12 @@ __global__ void __launch_bounds__(128) topk_kernel(
       const int e = j * 32 + lane;
       if (e < E) s[j] += __ldg(z + part * part_stride + e);
     }
+  }
+  if (row_scale != nullptr) {
+    const float f = __ldg(row_scale + token);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (j * 32 + lane < E) s[j] *= f;
   }
   if (score_fn == MOE_SCORE_SOFTMAX) {
     float m = -CUDART_INF_F;
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(128) topk_kernel(
 }
 
 cudaError_t launch_topk(const float* logits, const moe_params_t& p, const float* bias,
-                        int32_t* ids, float* w, cudaStream_t st, int n_part) {
+                        int32_t* ids, float* w, cudaStream_t st, int n_part, const float* row_scale) {
   const int grid = (p.T + 3) / 4;
   if (grid == 0) return cudaSuccess;
   const int epl = (p.E + 31) / 32;
@@ -306,7 +312,7 @@ cudaError_t launch_topk(const float* logits, const moe_params_t& p, const float*
 #define MOE_TOPK_CASE(N)                                                                             \
   err = launch_k(topk_kernel<N>, grid, 128, 0, st, logits, n_part, p.T, p.E, p.K, p.n_group,         \
                  p.topk_group, p.group_topn, static_cast<int>(p.score_fn), p.renormalize,            \
-                 p.routed_scale, bias, ids, w)
+                 p.routed_scale, bias, row_scale, ids, w)
   if (epl <= 1) MOE_TOPK_CASE(1);
   else if (epl <= 2) MOE_TOPK_CASE(2);
   else if (epl <= 4) MOE_TOPK_CASE(4);
@@ -583,9 +589,10 @@ __global__ void __launch_bounds__(1024) perm_small_kernel(
 //    One warp per row; each lane keeps up to 8 16-byte loads in flight, so the copy runs
 //    at HBM write speed rather than at the latency of one load per thread.
 constexpr int kGatherWarps = 8;
+//    FP8: x is 8-bit codes with nsc fp32 scales per row, copied to x_perm_scale.
 template <bool FP8>
 __global__ void __launch_bounds__(32 * kGatherWarps) perm_gather_kernel(
-    const void* __restrict__ x, const float* __restrict__ x_scale, int H, int K, int E,
+    const void* __restrict__ x, const float* __restrict__ x_scale, int nsc, int H, int K, int E,
     const int32_t* __restrict__ counts, const int32_t* __restrict__ offsets,
     int32_t* __restrict__ pair_of_row, void* __restrict__ x_perm,
     float* __restrict__ x_perm_scale, bool zero_pad) {
@@ -595,7 +602,6 @@ __global__ void __launch_bounds__(32 * kGatherWarps) perm_gather_kernel(
   const int total = __ldg(offsets + E);
   const int row_bytes = FP8 ? H : 2 * H;
   const int nvec = row_bytes / 16;
-  const int nsc = H / 128;
   const int warps = gridDim.x * kGatherWarps;
   for (int r = blockIdx.x * kGatherWarps + (threadIdx.x >> 5); r < total; r += warps) {
     int lo = 0, hi = E - 1;  // expert owning row r: smallest e with offsets[e+1] > r
@@ -637,7 +643,7 @@ __global__ void __launch_bounds__(32 * kGatherWarps) perm_gather_kernel(
 constexpr int kScatterWarps = 8;
 template <bool FP8>
 __global__ void __launch_bounds__(32 * kScatterWarps) perm_scatter_kernel(
-    const void* __restrict__ x, const float* __restrict__ x_scale, int T, int H, int K,
+    const void* __restrict__ x, const float* __restrict__ x_scale, int nsc, int T, int H, int K,
     const int32_t* __restrict__ row_of_pair, void* __restrict__ x_perm, float* __restrict__ x_perm_scale,
     uint8_t* __restrict__ x_atoms) {
   pdl_launch_dependents();
@@ -645,7 +651,6 @@ __global__ void __launch_bounds__(32 * kScatterWarps) perm_scatter_kernel(
   const int lane = threadIdx.x & 31;
   const int row_bytes = FP8 ? H : 2 * H;
   const int nvec = row_bytes / 16;
-  const int nsc = H / 128;
   const int nchunk = (nvec + 255) / 256;
   const long long units = static_cast<long long>(T) * nchunk;
   const int warps = gridDim.x * kScatterWarps;
@@ -711,6 +716,7 @@ cudaError_t launch_permute(const moe_params_t& p, int block_m, const int32_t* id
   const int P = p.T * p.K;
   const int nchunks = (P + kPermChunk - 1) / kPermChunk;
   const int bm = block_m;
+  const int nsc = x_scales_per_row(p);
   cudaError_t err;
   if (P > 0 && P <= kSmallPairs) {
     trace_before(MOE_K_PERM_SCAN, st);
@@ -743,16 +749,16 @@ cudaError_t launch_permute(const moe_params_t& p, int block_m, const int32_t* id
   const bool masked = p.masked_cap > 0;
   const bool zero_pad = !masked && fill_pad;
   if (!fill_pad && p.T > 0) {
-    const long long row_vecs = (act_e4m3(p) ? p.H : 2LL * p.H) / 16;
+    const long long row_vecs = (nsc > 0 ? p.H : 2LL * p.H) / 16;
     const long long units = static_cast<long long>(p.T) * ((row_vecs + 255) / 256);
     const long long want = (units + kScatterWarps - 1) / kScatterWarps;
     const int grid = static_cast<int>(want < num_sms() * 8LL ? want : num_sms() * 8LL);
     trace_before(MOE_K_PERM_GATHER, st);
-    if (act_e4m3(p))
-      err = launch_k(perm_scatter_kernel<true>, grid, 32 * kScatterWarps, 0, st, x, x_scale, p.T, p.H, p.K,
+    if (nsc > 0)
+      err = launch_k(perm_scatter_kernel<true>, grid, 32 * kScatterWarps, 0, st, x, x_scale, nsc, p.T, p.H, p.K,
                      row_of_pair, x_perm, x_perm_scale, x_atoms);
     else
-      err = launch_k(perm_scatter_kernel<false>, grid, 32 * kScatterWarps, 0, st, x, x_scale, p.T, p.H, p.K,
+      err = launch_k(perm_scatter_kernel<false>, grid, 32 * kScatterWarps, 0, st, x, x_scale, nsc, p.T, p.H, p.K,
                      row_of_pair, x_perm, x_perm_scale, static_cast<uint8_t*>(nullptr));
     trace_after(MOE_K_PERM_GATHER, st);
     return err != cudaSuccess ? err : cudaGetLastError();
@@ -762,11 +768,11 @@ cudaError_t launch_permute(const moe_params_t& p, int block_m, const int32_t* id
   const long long blocks = (max_rows + kGatherWarps - 1) / kGatherWarps;
   const int grid = static_cast<int>(blocks < num_sms() * 8LL ? (blocks > 0 ? blocks : 1) : num_sms() * 8LL);
   trace_before(MOE_K_PERM_GATHER, st);
-  if (act_e4m3(p))
-    err = launch_k(perm_gather_kernel<true>, grid, 32 * kGatherWarps, 0, st, x, x_scale, p.H, p.K, p.E, counts,
+  if (nsc > 0)
+    err = launch_k(perm_gather_kernel<true>, grid, 32 * kGatherWarps, 0, st, x, x_scale, nsc, p.H, p.K, p.E, counts,
                    offsets, pair_of_row, x_perm, x_perm_scale, zero_pad);
   else
-    err = launch_k(perm_gather_kernel<false>, grid, 32 * kGatherWarps, 0, st, x, x_scale, p.H, p.K, p.E, counts,
+    err = launch_k(perm_gather_kernel<false>, grid, 32 * kGatherWarps, 0, st, x, x_scale, nsc, p.H, p.K, p.E, counts,
                    offsets, pair_of_row, x_perm, x_perm_scale, zero_pad);
   trace_after(MOE_K_PERM_GATHER, st);
   return err != cudaSuccess ? err : cudaGetLastError();
@@ -1002,7 +1008,7 @@ cudaError_t launch_combine(const moe_params_t& p, const void* y_perm, const int3
     err = launch_combine_t<__half, float>(p, y_perm, row_of_pair, w, y_shared, out, st, grid, pieces);
   else if (ysh_f16)
     err = launch_combine_t<float, __half>(p, y_perm, row_of_pair, w, y_shared, out, st, grid, pieces);
-  else if (act_e4m3(p))
+  else if (act_e4m3(p) || act_i8(p))
     err = launch_combine_t<__nv_bfloat16, float>(p, y_perm, row_of_pair, w, y_shared, out, st, grid, pieces);
   else
     err = launch_combine_t<float, float>(p, y_perm, row_of_pair, w, y_shared, out, st, grid, pieces);

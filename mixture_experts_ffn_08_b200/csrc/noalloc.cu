@@ -69,7 +69,7 @@ extern "C" moe_status_t moe_permute_noalloc(const moe_params_t* p, const int32_t
   if ((!empty && (!topk_ids || !x || !row_of_pair)) || !counts || !offsets_padded || !pair_of_row || !x_perm)
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(x_perm)) return MOE_ERR_INVALID_ARG;
-  if (act_e4m3(*p) && ((!empty && !x_scale) || !x_perm_scale)) return MOE_ERR_INVALID_ARG;
+  if (x_scales_per_row(*p) > 0 && ((!empty && !x_scale) || !x_perm_scale)) return MOE_ERR_INVALID_ARG;
   const long long pairs = static_cast<long long>(p->T) * p->K;
   const long long chunks = (pairs + kPermChunk - 1) / kPermChunk;
   if ((chunks > 0 ? chunks : 1) * p->E > kNoAllocScratchInts) return MOE_ERR_UNSUPPORTED;

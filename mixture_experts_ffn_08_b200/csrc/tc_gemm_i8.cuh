@@ -1,0 +1,426 @@
+// Persistent, warp-specialised tcgen05 matrix product of 8-bit integers, dense or grouped by
+// expert, with one scale per row of A (a token) and one per row of B (an output channel):
+//
+//   out[r, n] = a_scale[r] * w_scale[n] * sum_k A[r, k] * B[n, k]  (+ bias[n])
+//   h[r, n]   = SiLU(g) * u, g and u two such products              (SWIGLU)
+//
+// The sums are exact: kind::i8 accumulates s8 products in s32, and the callers keep
+// K * 128 * 128 below 2^31.  The scales leave the sum, so they cost one multiplication per
+// output in the epilogue and the main loop is a plain int8 product at the e4m3 rate.
+//
+// CG = 1: a CTA computes 128 x BN tiles on its own.  CG = 2: a cluster of two CTAs computes a
+// 256 x BN tile with one stream of cta_group::2 MMAs, each CTA holding 128 rows of A and half
+// of the BN rows of B; the operand bytes that cross L2 -> SM per MAC are those of a 256 x 256
+// tile while each SM's TMEM still holds two accumulators, so the epilogue of one tile runs
+// under the main loop of the next.  (At K = 1536 a tile's MMAs last only 6000 cycles: an
+// epilogue that the main loop had to wait for would cost a third of that.)
+// A group's first row is a multiple of 128, not of 256: the second half of a group's last pair
+// tile may lie past the group, and then it is neither loaded nor stored.
+//
+// Rows: group g's real rows are the first count(g) of those that start at offsets[g] (or at
+// g * masked_cap).  The schedule comes from the counts alone: work items are (group, N-tile,
+// M-tile) with a prefix sum over the groups in shared memory, all of the same cost, and
+// walked in steps of the grid.
+//
+// Warp roles (192 threads): warp 0 issues TMA loads into the stage ring, warp 1 allocates TMEM
+// and issues MMAs, warps 2-5 run the epilogue.  Every wait is bounded; on a timeout the CTA
+// sets MOE_DEV_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
+#pragma once
+
+#include "tc_gemm_2cta.cuh"
+
+namespace moe {
+
+constexpr int kI8MaxGroups = 1024;
+constexpr int kI8SmallRows = 32;  // an M-tile of at most this many rows loads this many of A
+
+struct I8Params {
+  const int32_t* offsets;  // [G+1] first row of each group (contiguous layout, grouped)
+  const int32_t* counts;   // [G] real rows; nullptr: offsets[g+1] - offsets[g], or dense_rows
+  int G;
+  int dense_rows;          // > 0: one group of that many rows, offsets and counts unused
+  int masked_cap;          // > 0: group g's rows start at g * masked_cap
+  int K;                   // reduction length, a multiple of 16
+  int N;                   // output columns of a group
+  const float* a_scale;    // [rows of A]
+  const float* w_scale;    // [G * N]
+  const float* w_scale_up; // [G * N] (SWIGLU)
+  const float* bias;       // [N] or nullptr
+  void* out;               // SWIGLU: fp32 [rows, ldo]; else out_type
+  int out_type;            // moe_out_type_t
+  int64_t ldo;
+  int32_t* status;
+};
+
+// D format s32, A and B signed 8-bit, both K-major.
+__host__ __device__ constexpr uint32_t idesc_i8_s32(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <int CG>
+MOE_DEVINL void umma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+template <int CG_, int BN_, bool SWIGLU_, int STAGES_>
+struct I8Cfg {
+  static constexpr int CG = CG_;
+  static constexpr int BN = BN_;
+  static constexpr bool SWIGLU = SWIGLU_;
+  static constexpr int STAGES = STAGES_;
+  static constexpr int BK = 128;                 // codes per K-step: one 128-byte swizzle row
+  static constexpr int A_BYTES = 128 * BK;
+  static constexpr int B_ROWS = BN / CG;         // B rows held by each CTA
+  static constexpr int B_BYTES = B_ROWS * BK;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+  static constexpr int OUT_COLS = SWIGLU ? BN / 2 : BN;
+  static constexpr int TMEM_COLS = 2 * BN;       // two accumulators
+  static constexpr int TILE_M = 128 * CG;
+  static constexpr int THREADS = 192;
+  static_assert(BN == 32 || BN == 64 || BN == 128 || BN == 256, "two accumulators in a power of two of TMEM columns");
+  static_assert(!SWIGLU || BN == 256, "a SwiGLU tile is 128 gate and 128 up rows");
+  static_assert(CG == 1 || BN == 256, "pair tiles are 256 x 256");
+  static_assert(SMEM_BYTES + 4 * (kI8MaxGroups + 2) + 4 * 512 * 4 + 1024 <= 227 * 1024, "shared memory");
+};
+
+struct I8Tile {
+  int group;
+  int n_tile;
+  int m0;            // first row of the tile inside its group
+  int count;         // real rows of the group
+  long long row0;    // first row of the tile in A and out
+};
+
+MOE_DEVINL int i8_count(const I8Params& p, int g) {
+  if (p.dense_rows > 0) return p.dense_rows;
+  return p.counts != nullptr ? __ldg(p.counts + g) : __ldg(p.offsets + g + 1) - __ldg(p.offsets + g);
+}
+
+// Work item -> tile; pref[g] = NT * sum over e < g of M-tiles(e).  Inside a group the operand
+// with fewer rows is the one that the CTAs running side by side read again from L2.
+template <class Cfg>
+MOE_DEVINL I8Tile i8_decode(int item, int NT, const I8Params& p, const int* pref) {
+  int lo = 0, hi = p.G - 1;  // group with pref[g] <= item < pref[g+1]
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pref[mid] <= item) lo = mid; else hi = mid - 1;
+  }
+  I8Tile t;
+  t.group = lo;
+  t.count = i8_count(p, lo);
+  const int tiles = (t.count + Cfg::TILE_M - 1) / Cfg::TILE_M;
+  const int local = item - pref[lo];
+  const bool m_outer = static_cast<long long>(tiles) * Cfg::TILE_M > static_cast<long long>(NT) * Cfg::BN;
+  t.m0 = (m_outer ? local / NT : local % tiles) * Cfg::TILE_M;
+  t.n_tile = m_outer ? local % NT : local / tiles;
+  const long long first = p.dense_rows > 0 ? 0
+                          : p.masked_cap > 0 ? static_cast<long long>(lo) * p.masked_cap : __ldg(p.offsets + lo);
+  t.row0 = first + t.m0;
+  return t;
+}
+
+// Rows of A that a CTA loads for `rows` real rows from its half of the tile on.
+MOE_DEVINL int i8_box_rows(int rows) { return rows <= 0 ? 0 : (rows <= kI8SmallRows ? kI8SmallRows : 128); }
+
+// 32 fp32 outputs of one row, columns col .. col + 31 of which the first n are stored.
+MOE_DEVINL void i8_store32(const I8Params& p, long long row, int col, const float (&v)[32], int n) {
+  const long long at = row * p.ldo + col;
+  if (p.out_type == MOE_OUT_FP32) {
+    float* o = static_cast<float*>(p.out) + at;
+    if (n >= 32 && (reinterpret_cast<uintptr_t>(o) & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st_global_v8(o + 8 * i, reinterpret_cast<const uint32_t*>(v) + 8 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < n) o[i] = v[i];
+    }
+    return;
+  }
+  uint32_t w[16];
+  if (p.out_type == MOE_OUT_BF16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const __half2 hv = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&hv);
+    }
+  }
+  uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+  if (n >= 32 && (reinterpret_cast<uintptr_t>(o) & 31) == 0) {
+    st_global_v8(o, w);
+    st_global_v8(o + 16, w + 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < n) o[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+// tmA: boxes of 128 rows of A, tmA32: of 32.  tmB0 (and tmB1, the up weights of SWIGLU): boxes
+// of B_ROWS rows, or of 128 for SWIGLU.
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+    tc_gemm_i8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+                      const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+                      const I8Params p) {
+  constexpr int CG = Cfg::CG, BN = Cfg::BN, BK = Cfg::BK, STAGES = Cfg::STAGES;
+  constexpr bool PAIR = CG == 2;
+  constexpr uint32_t IDESC = idesc_i8_s32(Cfg::TILE_M, BN);
+
+  extern __shared__ uint8_t dsmem[];
+  __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES];
+  __shared__ uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
+  __shared__ int pref[kI8MaxGroups + 1];
+  __shared__ __align__(16) float col_sh[4][512];  // per epilogue warp: column scales, then biases
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ volatile int abort_flag;
+  __shared__ int no_abort_sh[2];
+
+  const int warp = warp_id(), lane = lane_id();
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const uint32_t pad = (1024u - (smem_u32(dsmem) & 1023u)) & 1023u;
+  uint8_t* smem = dsmem + pad;
+  const int NT = (p.N + Cfg::OUT_COLS - 1) / Cfg::OUT_COLS;
+  const int KB = (p.K + BK - 1) / BK;
+  const int first_item = blockIdx.x / CG, step = gridDim.x / CG;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull_bar[a], 1);
+      mbar_init(&tempty_bar[a], 4 * CG);  // one lane of each epilogue warp
+    }
+    mbar_init(&drain_bar, 1);
+    abort_flag = 0;
+    no_abort_sh[0] = no_abort_sh[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmA32);
+    prefetch_tmap(&tmB0);
+    if (Cfg::SWIGLU) prefetch_tmap(&tmB1);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(&tmem_base_sh, Cfg::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&tmem_base_sh, Cfg::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  // the counts and A come from the kernels before this one
+  pdl_launch_dependents();
+  pdl_wait();
+  if (warp == 2) {
+    // pref[] over the groups, one warp: each lane sums a contiguous run, then a scan
+    const int per = (p.G + 31) / 32;
+    const int g0 = lane * per;
+    int run = 0;
+    for (int g = g0; g < g0 + per && g < p.G; ++g) run += NT * ((i8_count(p, g) + Cfg::TILE_M - 1) / Cfg::TILE_M);
+    int incl = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int acc = incl - run;
+    for (int g = g0; g < g0 + per && g < p.G; ++g) {
+      pref[g] = acc;
+      acc += NT * ((i8_count(p, g) + Cfg::TILE_M - 1) / Cfg::TILE_M);
+    }
+    if (lane == 31) pref[p.G] = incl;
+  }
+  __syncwarp();
+  tc_fence_before();
+  if constexpr (PAIR) cluster_sync(); else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_sh;
+  const int total = pref[p.G];
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (int item = first_item; item < total && ok; item += step) {
+        const I8Tile t = i8_decode<Cfg>(item, NT, p, pref);
+        const int a_box = i8_box_rows(t.count - t.m0 - 128 * static_cast<int>(rank));
+        uint32_t tx = static_cast<uint32_t>(a_box) * BK + Cfg::B_BYTES;
+        if (PAIR) tx += static_cast<uint32_t>(i8_box_rows(t.count - t.m0 - 128)) * BK + Cfg::B_BYTES;  // (the leader's)
+        const int a_row = static_cast<int>(t.row0) + 128 * static_cast<int>(rank);
+        const int b_row = t.group * p.N + t.n_tile * Cfg::OUT_COLS +
+                          (PAIR && !Cfg::SWIGLU ? static_cast<int>(rank) * Cfg::B_ROWS : 0);
+        const CUtensorMap* mA = a_box == kI8SmallRows ? &tmA32 : &tmA;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait_bounded(&empty_bar[s], ph ^ 1u, &abort_flag)) { ok = false; break; }
+          uint8_t* sa = smem + s * Cfg::STAGE_BYTES;
+          uint8_t* sb = sa + Cfg::A_BYTES;
+          if constexpr (PAIR) {
+            const uint32_t bar = mapa_shared(smem_u32(&full_bar[s]), 0);
+            if (leader) mbar_arrive_expect_tx(&full_bar[s], tx);
+            if (a_box > 0) tma_load_2d_pair(sa, mA, kb * BK, a_row, bar);
+            tma_load_2d_pair(sb, (Cfg::SWIGLU && rank == 1) ? &tmB1 : &tmB0, kb * BK, b_row, bar);
+          } else {
+            mbar_arrive_expect_tx(&full_bar[s], tx);
+            tma_load_2d(sa, mA, kb * BK, a_row, &full_bar[s]);
+            tma_load_2d(sb, &tmB0, kb * BK, b_row, &full_bar[s]);
+            if constexpr (Cfg::SWIGLU) tma_load_2d(sb + Cfg::B_BYTES / 2, &tmB1, kb * BK, b_row, &full_bar[s]);
+          }
+          ++issued;
+          if (++s == STAGES) { s = 0; ph ^= 1u; }
+        }
+      }
+      if (leader) {
+        // (the leader's stage barriers count the peer's bytes too)
+        volatile int* no_abort = &no_abort_sh[0];
+        const long long back = issued < STAGES ? issued : STAGES;
+        for (long long j = 0; j < back; ++j) {
+          if (s == 0) { s = STAGES - 1; ph ^= 1u; } else { --s; }
+          mbar_wait_bounded(&full_bar[s], ph, no_abort);
+        }
+        if (*no_abort) abort_flag = 1;
+      }
+      if (!ok) abort_flag = 1;
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA (the leader's)
+    if (leader && lane == 0) {
+      int s = 0, acc = 0;
+      uint32_t ph = 0, acc_ph = 0;
+      bool ok = true;
+      for (int item = first_item; item < total && ok; item += step) {
+        if (!mbar_wait_bounded(&tempty_bar[acc], acc_ph ^ 1u, &abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * BN;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait_bounded(&full_bar[s], ph, &abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + s * Cfg::STAGE_BYTES);
+          const uint32_t b0 = a0 + Cfg::A_BYTES;
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)
+            umma_i8<CG>(d_tmem, smem_desc_sw128(a0 + k * 32), smem_desc_sw128(b0 + k * 32), IDESC, (kb | k) != 0);
+          if constexpr (PAIR) umma_commit_pair(&empty_bar[s]); else umma_commit(&empty_bar[s]);
+          if (++s == STAGES) { s = 0; ph ^= 1u; }
+        }
+        if (!ok) break;
+        if constexpr (PAIR) umma_commit_pair(&tfull_bar[acc]); else umma_commit(&tfull_bar[acc]);
+        if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
+      }
+      if constexpr (PAIR) umma_commit_pair_local(&drain_bar); else umma_commit(&drain_bar);
+      volatile int* no_abort = &no_abort_sh[1];
+      mbar_wait_bounded(&drain_bar, 0, no_abort);
+      if (!ok || *no_abort) abort_flag = 1;
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp & 3;  // TMEM lane quadrant
+    float* cols = col_sh[q];
+    const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&tempty_bar[0]), 0) : 0u;
+    const uint32_t tempty1 = PAIR ? mapa_shared(smem_u32(&tempty_bar[1]), 0) : 0u;
+    int acc = 0;
+    uint32_t acc_ph = 0;
+    for (int item = first_item; item < total; item += step) {
+      const I8Tile t = i8_decode<Cfg>(item, NT, p, pref);
+      const int col0 = t.n_tile * Cfg::OUT_COLS;
+      const long long wrow = static_cast<long long>(t.group) * p.N + col0;
+      const int in_tile = 128 * static_cast<int>(rank) + q * 32 + lane;
+      const long long row = t.row0 + in_tile;
+      const bool row_ok = t.m0 + in_tile < t.count;
+      const float sa = row_ok ? __ldg(p.a_scale + row) : 0.f;
+      __syncwarp();
+      for (int c = lane; c < Cfg::OUT_COLS; c += 32) {
+        const bool in = col0 + c < p.N;
+        cols[c] = in ? __ldg(p.w_scale + wrow + c) : 0.f;
+        if constexpr (Cfg::SWIGLU) cols[128 + c] = in ? __ldg(p.w_scale_up + wrow + c) : 0.f;
+        else cols[256 + c] = in && p.bias != nullptr ? __ldg(p.bias + col0 + c) : 0.f;
+      }
+      __syncwarp();
+      const bool ready = __all_sync(0xffffffffu, mbar_wait_bounded(&tfull_bar[acc], acc_ph, &abort_flag));
+      if (!ready) break;
+      tc_fence_after();
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
+      if constexpr (Cfg::SWIGLU) {
+        float* out = static_cast<float*>(p.out) + row * p.ldo + col0;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t rg[32], ru[32];
+          tmem_ld_32x32b_x32(tbase + c, rg);
+          tmem_ld_32x32b_x32(tbase + 128 + c, ru);
+          tmem_ld_wait(rg);
+          reg_fence(ru);
+          if (row_ok) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float g = __int2float_rn(static_cast<int>(rg[i])) * (sa * cols[c + i]);
+              const float u = __int2float_rn(static_cast<int>(ru[i])) * (sa * cols[128 + c + i]);
+              rg[i] = __float_as_uint(silu_mul(g, u));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_global_v8(out + c + 8 * i, rg + 8 * i);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(tbase + c, r);
+          tmem_ld_wait(r);
+          if (row_ok && col0 + c < p.N) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              v[i] = fmaf(__int2float_rn(static_cast<int>(r[i])), sa * cols[c + i], cols[256 + c + i]);
+            i8_store32(p, row, col0 + c, v, p.N - col0 - c);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(acc == 0 ? tempty0 : tempty1);
+        else mbar_arrive(&tempty_bar[acc]);
+      }
+      if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
+    }
+  }
+
+  __syncthreads();
+  tc_fence_before();
+  if constexpr (PAIR) cluster_sync();  // both CTAs done with TMEM and with each other's barriers
+  tc_fence_after();
+  if (abort_flag && threadIdx.x == 0) set_status(p.status, MOE_DEV_TIMEOUT);
+  if (warp == 1) {
+    __syncwarp();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, Cfg::TMEM_COLS);
+    else tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+  }
+}
+
+}  // namespace moe

@@ -18,7 +18,7 @@ import math
 
 import torch
 
-from .workloads import Workload, DTYPE_FP8, DTYPE_FP8_FP4
+from .workloads import Workload, DTYPE_FP8, DTYPE_FP8_FP4, DTYPE_INT8
 
 _TAGS = {"x": 1, "w_r": 2, "bias": 3, "w_gate": 4, "w_up": 5, "w_down": 6,
          "ws_gate": 7, "ws_up": 8, "ws_down": 9, "skew_m": 10, "skew_rank": 11}
@@ -80,6 +80,15 @@ def quantize_blocks_e4m3(v: torch.Tensor, rows_per_block: int):
     return q.view(torch.uint8), s.contiguous()
 
 
+def quantize_rows_int8(v: torch.Tensor):
+    """Encode a [R, C] fp32 matrix as int8 codes with one scale per row, max|v| / 127 (1 where
+    the row is zero), nearest code with ties to even.  Returns (codes int8 [R, C], scales fp32
+    [R]).  This is how the int8 workload's given inputs are produced."""
+    amax = v.abs().amax(dim=1)
+    s = torch.where(amax > 0, amax / 127.0, torch.ones_like(amax))
+    return torch.round(v / s[:, None]).clamp_(-127, 127).to(torch.int8), s.contiguous()
+
+
 FP4_MAX = 6.0
 FP4_BLOCK = 32
 # The eight non-negative e2m1 values (OCP MX FP4), in code order 0..7.
@@ -121,6 +130,15 @@ def _stacked_fp4(n, rows, cols, g, device):
     return packed, scales
 
 
+def _stacked_int8(n, rows, cols, g, device):
+    codes = torch.empty((n, rows, cols), dtype=torch.int8, device=device)
+    scales = torch.empty((n, rows), dtype=torch.float32, device=device)
+    for e in range(n):
+        w = torch.randn((rows, cols), generator=g, device=device, dtype=torch.float32) * WEIGHT_STD
+        codes[e], scales[e] = quantize_rows_int8(w)
+    return codes, scales
+
+
 def _stacked_fp8(n, rows, cols, g, device):
     codes = torch.empty((n, rows, cols), dtype=torch.uint8, device=device)
     scales = torch.empty((n, rows // QBLOCK, cols // QBLOCK), dtype=torch.float32, device=device)
@@ -139,7 +157,8 @@ def make_inputs(wl: Workload, seed: int = 0, device="cpu", weights: bool = True)
     FP8 workload: x is replaced by x_q [T,H] uint8 (e4m3 codes) + x_scale
     [T,H/128] fp32, and each expert weight W by W_q uint8 + W_s fp32
     [E, rows/128, cols/128].  FP8 x FP4 workload: x as for FP8; W_q is packed e2m1
-    uint8 [E, rows, cols/2] and W_s UE8M0 bytes uint8 [E, rows, cols/32].  With
+    uint8 [E, rows, cols/2] and W_s UE8M0 bytes uint8 [E, rows, cols/32].  Int8 workload:
+    x_q int8 [T,H] + x_scale fp32 [T], W_q int8 + W_s fp32 [E, rows].  With
     weights=False only x (and the router) are drawn.
     """
     T, H, I, E = wl.T, wl.H, wl.I, wl.E
@@ -154,6 +173,8 @@ def make_inputs(wl: Workload, seed: int = 0, device="cpu", weights: bool = True)
         x = torch.randn((T, H), generator=g, device=device, dtype=torch.float32)
     if wl.dtype in (DTYPE_FP8, DTYPE_FP8_FP4):
         out["x_q"], out["x_scale"] = quantize_blocks_e4m3(x, 1)
+    elif wl.dtype == DTYPE_INT8:
+        out["x_q"], out["x_scale"] = quantize_rows_int8(x)
     else:
         out["x"] = x.to(torch.bfloat16)
     del x
@@ -179,6 +200,9 @@ def make_inputs(wl: Workload, seed: int = 0, device="cpu", weights: bool = True)
     if wl.dtype == DTYPE_FP8:
         for name, rows, cols in (("w_gate", I, H), ("w_up", I, H), ("w_down", H, I)):
             out[name + "_q"], out[name + "_s"] = _stacked_fp8(E, rows, cols, _gen(device, seed, name), device)
+    elif wl.dtype == DTYPE_INT8:
+        for name, rows, cols in (("w_gate", I, H), ("w_up", I, H), ("w_down", H, I)):
+            out[name + "_q"], out[name + "_s"] = _stacked_int8(E, rows, cols, _gen(device, seed, name), device)
     elif wl.dtype == DTYPE_FP8_FP4:
         for name, rows, cols in (("w_gate", I, H), ("w_up", I, H), ("w_down", H, I)):
             out[name + "_q"], out[name + "_s"] = _stacked_fp4(E, rows, cols, _gen(device, seed, name), device)

@@ -18,6 +18,7 @@ SCORE_SIGMOID = 1
 DTYPE_BF16 = 0
 DTYPE_FP8 = 1
 DTYPE_FP8_FP4 = 2      # e4m3 activations, e2m1 weights with UE8M0 scales per 32 K elements
+DTYPE_INT8 = 3         # int8 activations with a scale per token, int8 weights with a scale per output channel
 
 
 @dataclass(frozen=True)

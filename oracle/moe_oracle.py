@@ -125,6 +125,36 @@ def quantize_rows_1x128(h) -> np.ndarray:
 
 
 # ----------------------------------------------------------------------------------
+# int8 codes with one scale per row, and the norm in front of the layer
+# ----------------------------------------------------------------------------------
+def dequant_rows(codes, scales) -> np.ndarray:
+    """codes [R, C] int8 with scales [R] -> float64 [R, C]."""
+    return np.asarray(codes, np.float64) * np.asarray(scales, np.float64)[:, None]
+
+
+def int8_scale(amax) -> np.ndarray:
+    """amax / 127, 1 where amax is 0."""
+    a = np.asarray(amax, np.float64)
+    return np.where(a > 0, a / 127.0, 1.0)
+
+
+def quantize_rows_int8(h) -> np.ndarray:
+    """Re-quantise [R, C] to int8 with one scale per row, max|h| / 127; nearest code, ties to
+    even.  Returns the dequantised float64 values."""
+    h = np.asarray(h, np.float64)
+    s = int8_scale(np.abs(h).max(axis=1))[:, None]
+    return np.round(h / s) * s
+
+
+def add_rms_norm(x, residual, w, eps: float):
+    """(z, y) of z = bf16(x + residual) (x without one) and y = z / sqrt(mean(z^2) + eps) * w."""
+    z = np.asarray(x, np.float64)
+    if residual is not None:
+        z = round_bf16(z + np.asarray(residual, np.float64))
+    return z, z / np.sqrt((z * z).mean(axis=1, keepdims=True) + eps) * np.asarray(w, np.float64)[None, :]
+
+
+# ----------------------------------------------------------------------------------
 # e2m1 (OCP MX FP4) weights with one UE8M0 scale per 32 consecutive K elements: the
 # FP4 operand of the FP8 x FP4 GEMM ("DeepGEMM质变", §5.3; §一 1.3 for the UE8M0
 # scale buffers of the FP4 path)
@@ -163,13 +193,15 @@ def round_bf16(v) -> np.ndarray:
 
 
 def store_activation(h, h_format):
-    """h in the activation format of the layer: None (exact), "bf16" or "e4m3"."""
+    """h in the activation format of the layer: None (exact), "bf16", "e4m3" or "int8"."""
     if h_format is None:
         return np.asarray(h, np.float64)
     if h_format == "bf16":
         return round_bf16(h)
     if h_format == "e4m3":
         return quantize_rows_1x128(h)
+    if h_format == "int8":
+        return quantize_rows_int8(h)
     raise ValueError(h_format)
 
 
@@ -376,7 +408,10 @@ def forward_given_routing(x, ids, w, expert_weights, E: int, shared=None,
 
 def activation_format(dtype: int):
     """Storage format of h for a workload dtype: 0 = bf16; 1 (FP8) and 2 (FP8 x FP4, whose
-    FP4 operand is the weights) have e4m3 activations, so h is e4m3 with 1x128 scales."""
+    FP4 operand is the weights) have e4m3 activations, so h is e4m3 with 1x128 scales; 3 = int8
+    with one scale per row."""
+    if dtype == 3:
+        return "int8"
     return "e4m3" if dtype in (1, 2) else "bf16"
 
 
