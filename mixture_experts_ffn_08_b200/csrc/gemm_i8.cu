@@ -35,17 +35,40 @@ bool make_tmap_i8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Output [rows, cols] of 2- or 4-byte elements, row stride ld elements: boxes of 32 rows x 128
+// bytes.  False where the rows do not start and end on 16-byte borders (the store unit clips a box
+// at such a border: it was seen to write past cols); the kernel then stores element by element.
+bool make_tmap_out(CUtensorMap* m, void* ptr, uint64_t rows, uint64_t cols, uint64_t ld, bool wide) {
+  auto fn = encode_fn_i8();
+  const uint64_t esz = wide ? 4 : 2;
+  if (fn == nullptr || (reinterpret_cast<uintptr_t>(ptr) & 15u) != 0 || ld * esz % 16 != 0 || cols * esz % 16 != 0 ||
+      ld * esz >= (1ull << 40))
+    return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld * esz};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esz), 32};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, wide ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, ptr, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
 // A [a_rows, K] (row stride lda), B [b_rows, K] (row stride ldb; b1: SWIGLU's up weights).
 template <class Cfg>
 cudaError_t launch_i8(const void* A, int64_t a_rows, int64_t lda, const void* b0, const void* b1, int64_t b_rows,
-                      int64_t ldb, const I8Params& p, long long max_items, int kid, cudaStream_t st) {
+                      int64_t ldb, I8Params p, long long max_items, int kid, cudaStream_t st) {
   constexpr uint32_t b_box = Cfg::SWIGLU ? 128 : Cfg::B_ROWS;
   CUtensorMap ta, ta32, tb0, tb1;
   if (!make_tmap_i8(&ta, A, a_rows, p.K, lda, 128) || !make_tmap_i8(&ta32, A, a_rows, p.K, lda, kI8SmallRows) ||
       !make_tmap_i8(&tb0, b0, b_rows, p.K, ldb, b_box) || !make_tmap_i8(&tb1, b1, b_rows, p.K, ldb, b_box))
     return cudaErrorInvalidValue;
+  CUtensorMap tout;
+  const bool wide = Cfg::SWIGLU || p.out_type == MOE_OUT_FP32;
+  // (a 16-bit box is 64 columns wide, more than the narrowest tile)
+  p.tma_store = (wide || Cfg::BN >= 64) && make_tmap_out(&tout, p.out, a_rows, p.N, p.ldo, wide) ? 1 : 0;
+  if (!p.tma_store) tout = ta;  // never used then
   auto kern = tc_gemm_i8_kernel<Cfg>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
   if (err != cudaSuccess) return err;
@@ -73,7 +96,7 @@ cudaError_t launch_i8(const void* A, int64_t a_rows, int64_t lda, const void* b0
   cfg.attrs = attr;
   cfg.numAttrs = na;
   trace_before(kid, st);
-  err = cudaLaunchKernelEx(&cfg, kern, ta, ta32, tb0, tb1, p);
+  err = cudaLaunchKernelEx(&cfg, kern, ta, ta32, tb0, tb1, tout, p);
   trace_after(kid, st);
   return err != cudaSuccess ? err : cudaGetLastError();
 }
@@ -251,8 +274,8 @@ cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, cons
   if (mt * cdiv(N, 128) >= sms)
     return launch_i8<I8Cfg<1, 128, false, 6>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 128), MOE_K_LINEAR, st);
   if (mt * cdiv(N, 64) >= sms)
-    return launch_i8<I8Cfg<1, 64, false, 8>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 64), MOE_K_LINEAR, st);
-  return launch_i8<I8Cfg<1, 32, false, 9>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 32), MOE_K_LINEAR, st);
+    return launch_i8<I8Cfg<1, 64, false, 7>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 64), MOE_K_LINEAR, st);
+  return launch_i8<I8Cfg<1, 32, false, 8>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 32), MOE_K_LINEAR, st);
 }
 
 }  // namespace moe
