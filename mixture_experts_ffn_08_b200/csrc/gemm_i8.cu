@@ -101,6 +101,46 @@ cudaError_t launch_i8(const void* A, int64_t a_rows, int64_t lda, const void* b0
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
+// One tile per cluster of ks CTAs; A's boxes hold 32 rows where M is at most that.
+template <class Cfg>
+cudaError_t launch_i8_split(const void* a, int64_t lda, const void* w, int64_t ldw, const I8Params& p, int ks,
+                            cudaStream_t st) {
+  const int M = p.dense_rows, box = M <= kI8SmallRows ? kI8SmallRows : 128;
+  CUtensorMap ta, tb;
+  if (!make_tmap_i8(&ta, a, M, p.K, lda, box) || !make_tmap_i8(&tb, w, p.N, p.K, ldw, Cfg::BN))
+    return cudaErrorInvalidValue;
+  auto kern = tc_gemm_i8_split_kernel<Cfg>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ks, static_cast<unsigned>(cdiv(p.N, Cfg::BN)), static_cast<unsigned>(cdiv(M, 128)));
+  cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  trace_before(MOE_K_LINEAR, st);
+  err = cudaLaunchKernelEx(&cfg, kern, ta, tb, box, p);
+  trace_after(MOE_K_LINEAR, st);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <int M>
+cudaError_t launch_i8_gemv(const void* a, int64_t lda, const void* w, int64_t ldw, const I8Params& p, cudaStream_t st) {
+  trace_before(MOE_K_LINEAR, st);
+  const cudaError_t err = launch_k(i8_gemv_kernel<M>, static_cast<int>(cdiv(p.N, 8)), 256, 0, st,
+                                   static_cast<const int8_t*>(a), lda, static_cast<const int8_t*>(w), ldw, p);
+  trace_after(MOE_K_LINEAR, st);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
 // ------------------------------------------------------------------ h -> int8
 // q = rint(h / s), s = max|h| / 127 over the row (1 where the row is zero), as int8 codes and one
 // fp32 scale per row.  A row with a NaN or an infinity gets codes 0 and scale NaN, so that its
@@ -266,16 +306,39 @@ cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, cons
   p.out_type = out_type;
   p.ldo = ldo;
   p.status = status;
+  switch (M) {
+    case 1: return launch_i8_gemv<1>(a, lda, w, ldw, p, st);
+    case 2: return launch_i8_gemv<2>(a, lda, w, ldw, p, st);
+    case 3: return launch_i8_gemv<3>(a, lda, w, ldw, p, st);
+    case 4: return launch_i8_gemv<4>(a, lda, w, ldw, p, st);
+    default: break;
+  }
   const long long sms = num_sms();
-  // pair tiles where they fill the SMs, else the widest one-SM tile that does
-  if (cdiv(M, 256) * cdiv(N, 256) >= sms / 2)
-    return launch_i8<I8Cfg<2, 256, false, 6>>(a, M, lda, w, w, N, ldw, p, cdiv(M, 256) * cdiv(N, 256), MOE_K_LINEAR, st);
-  const long long mt = cdiv(M, 128);
-  if (mt * cdiv(N, 128) >= sms)
+  const long long mt = cdiv(M, 128), pairs = cdiv(M, 256) * cdiv(N, 256);
+  // pair tiles where they fill the SMs
+  if (pairs >= sms / 2)
+    return launch_i8<I8Cfg<2, 256, false, 6>>(a, M, lda, w, w, N, ldw, p, pairs, MOE_K_LINEAR, st);
+  // more 128 x 128 tiles than SMs: persistent one-SM tiles
+  if (mt * cdiv(N, 128) > sms)
     return launch_i8<I8Cfg<1, 128, false, 6>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 128), MOE_K_LINEAR, st);
-  if (mt * cdiv(N, 64) >= sms)
-    return launch_i8<I8Cfg<1, 64, false, 7>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 64), MOE_K_LINEAR, st);
-  return launch_i8<I8Cfg<1, 32, false, 8>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 32), MOE_K_LINEAR, st);
+  // One round of tiles of 128 x bn over ks parts of K each: of those that fit, the one whose CTAs
+  // load the fewest operand bytes; exchanging the parts counts as 32 KB per CTA.
+  const int KB = static_cast<int>(cdiv(K, 128)), box = M <= kI8SmallRows ? kI8SmallRows : 128;
+  int best_bn = 128, best_ks = 1;
+  long long best = -1;
+  for (int bn = 32; bn <= 128; bn *= 2)
+    for (int ks = 1; ks <= 8 && ks * 2 <= KB + 1; ks *= 2) {
+      if (mt * cdiv(N, bn) * ks > sms) continue;
+      const long long cost = static_cast<long long>(box + bn) * 128 * cdiv(KB, ks) + (ks > 1 ? 32768 : 0);
+      if (best < 0 || cost < best) {
+        best = cost;
+        best_bn = bn;
+        best_ks = ks;
+      }
+    }
+  if (best_bn == 32) return launch_i8_split<I8SplitCfg<32, 10>>(a, lda, w, ldw, p, best_ks, st);
+  if (best_bn == 64) return launch_i8_split<I8SplitCfg<64, 8>>(a, lda, w, ldw, p, best_ks, st);
+  return launch_i8_split<I8SplitCfg<128, 6>>(a, lda, w, ldw, p, best_ks, st);
 }
 
 }  // namespace moe

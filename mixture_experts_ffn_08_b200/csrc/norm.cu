@@ -12,8 +12,14 @@
 // rstd times it; the int8 codes, y / s = z w 127 / max|z w|, do not depend on rstd at all.
 // The sum runs in fp32 over 8 channels and in fp64 beyond, and rstd takes one Newton step in
 // fp64: a scale that is a power of two, or a code, changes where the true value lies within
-// 1e-7 of a border and not within 1e-6.  What bounds it is HBM: it reads x and the residual and
-// writes the sum and the output once each.
+// 1e-7 of a border and not within 1e-6.
+//
+// What bounds it is HBM: it reads x and the residual and writes the sum and the output once
+// each.  Blocks are persistent: while a row is reduced and stored, the block's next row is on its
+// way into shared memory (cp.async; every thread copies and reads back its own 16-byte vectors,
+// so nothing waits for anybody but the reduction).  About six instructions per channel: the sum
+// is one bf16x2 addition per pair, products and sums of squares are packed fp32 pairs, an int8
+// code is the low byte of one multiply-add onto 1.5 * 2^23.
 #include <cuda_fp8.h>
 #include <math_constants.h>
 
@@ -40,30 +46,55 @@ struct NormParams {
   double inv_h;          // 1 / H
 };
 
-MOE_DEVINL void unpack8(uint4 q, float (&f)[8]) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-MOE_DEVINL uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
-
-// |v| as an integer: the order of the values, infinities above them and NaN above those.
-MOE_DEVINL uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// (|v| as an integer keeps the order of the values, infinities above them and NaN above those)
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-// Smallest e >= -126 with v <= 448 * 2^e, for finite v > 0 (448 = 1.75 * 2^8).
-MOE_DEVINL int e4m3_exponent(double v) {
-  const int hi = __double2hiint(v), lo = __double2loint(v);
-  const int mant = hi & 0xfffff;
-  const int e = ((hi >> 20) & 0x7ff) - 1023 - 8 + ((mant > 0xc0000 || (mant == 0xc0000 && lo != 0)) ? 1 : 0);
-  return e < -126 ? -126 : (e > 127 ? 127 : e);
+// Biased exponent (e + 127, at least 1) of the smallest 2^e with v <= 448 * 2^e, for the value
+// v = m * rstd > 0 (448 = 1.75 * 2^8: a significand above 1.75 carries into the exponent).
+// Next to that border the fp32 product decides nothing, and the fp64 one does.
+MOE_DEVINL int e4m3_scale_bits(float m, float rstd_f, double rstd) {
+  const uint32_t b = __float_as_uint(m * rstd_f);
+  int e = static_cast<int>((b + 0x1fffffu) >> 23) - 8;
+  if (((b - 0x5ffff8u) & 0x7fffffu) < 16u || b < 0x00800000u) {
+    const double v = static_cast<double>(m) * rstd;
+    const int hi = __double2hiint(v), lo = __double2loint(v);
+    const int mant = hi & 0xfffff;
+    e = ((hi >> 20) & 0x7ff) - 1023 + 127 - 8 + ((mant > 0xc0000 || (mant == 0xc0000 && lo != 0)) ? 1 : 0);
+  }
+  return e < 1 ? 1 : e;
+}
+
+// Packed fp32 pairs.
+MOE_DEVINL float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return r;
+}
+MOE_DEVINL float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+        "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return r;
+}
+// max(a, |b|), NaN where either is.
+MOE_DEVINL float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+MOE_DEVINL float2 unpack2(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+// bf16(a + b) of two pairs.
+MOE_DEVINL uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 s = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&s);
+}
+MOE_DEVINL uint4 add8(uint4 a, uint4 b) {
+  return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
+}
+MOE_DEVINL void cp_async16(void* dst_smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst_smem)), "l"(src) : "memory");
 }
 
 MOE_DEVINL uint32_t codes_e4m3(const float* v) {
@@ -98,9 +129,10 @@ MOE_DEVINL double rsqrt_newton(double m) {
   return m < 3.0e38 ? r * (1.5 - 0.5 * m * r * r) : r;
 }
 
-// What a row's elements are multiplied with, and how.
+// What a row's products z w are multiplied with, and how.
 struct RowScale {
-  float factor;      // bf16: rstd; e4m3: rstd; int8: 127 / max |z w|
+  float factor;      // bf16 and e4m3: rstd; int8: 127 / max |z w|
+  float rest;        // e4m3: rstd - factor, so that a code sees one rounding
   double rstd;
   bool bad;          // e4m3, int8: a NaN, an infinity or a sum past fp32 in the row: scale NaN, codes 0
   bool wide;         // int8: `factor` does not fit fp32 well, multiply in fp64
@@ -112,12 +144,14 @@ MOE_DEVINL RowScale row_scale(double ss, uint32_t amax_bits, const NormParams& p
   RowScale r;
   r.rstd = rsqrt_newton(ss * p.inv_h + static_cast<double>(p.eps));
   r.factor = static_cast<float>(r.rstd);
+  r.rest = static_cast<float>(r.rstd - static_cast<double>(r.factor));
   r.bad = false;
   r.wide = false;
   r.factor_wide = 0.0;
-  if constexpr (FMT != NORM_BF16) r.bad = !(ss < 3.0e38) || amax_bits >= kInfBits;
+  if constexpr (FMT != NORM_BF16) r.bad = !(ss < 3.0e38);
   if constexpr (FMT == NORM_INT8) {
     const float amax = __uint_as_float(amax_bits);
+    r.bad = r.bad || amax_bits >= kInfBits;
     float s = 1.f;
     r.factor = 0.f;
     if (r.bad) {
@@ -137,129 +171,202 @@ MOE_DEVINL RowScale row_scale(double ss, uint32_t amax_bits, const NormParams& p
 
 // Stores the 8 outputs of vector v (products zw) of a row; called by whole half-warps.
 template <int FMT>
-MOE_DEVINL void store_vec(const float (&zw)[8], const RowScale& r, const NormParams& p, long long row, int v) {
+MOE_DEVINL void store_vec(const float2 (&zw)[4], const RowScale& r, const NormParams& p, long long row, int v) {
   const long long at = row * p.nvec + v;
   if constexpr (FMT == NORM_BF16) {
-    float y[8];
+    const float2 f = make_float2(r.factor, r.factor);
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = zw[i] * r.factor;
-    static_cast<uint4*>(p.out)[at] = pack8(y);
+    for (int i = 0; i < 4; ++i) {
+      const float2 y = mul2(zw[i], f);
+      w[i] = pack_bf16x2(y.x, y.y);
+    }
+    static_cast<uint4*>(p.out)[at] = make_uint4(w[0], w[1], w[2], w[3]);
   } else if constexpr (FMT == NORM_E4M3) {
-    uint32_t m = 0;
+    float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(zw[i]));
-    m = __reduce_max_sync(0xffffu << (threadIdx.x & 16), m);  // 16 lanes hold the 128 channels
-    float y[8];
+    for (int i = 0; i < 4; ++i) m = max_abs(max_abs(m, zw[i].x), zw[i].y);
+    // 16 lanes hold the 128 channels
+    m = __uint_as_float(__reduce_max_sync(0xffffu << (threadIdx.x & 16), __float_as_uint(m)));
+    float2 y[4];
     float s = 1.f;
-    if (r.bad) {
+    if (r.bad || __float_as_uint(m) >= kInfBits) {
       s = CUDART_NAN_F;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = 0.f;
+      for (int i = 0; i < 4; ++i) y[i] = make_float2(0.f, 0.f);
     } else {
-      const int e = m > 0 ? e4m3_exponent(static_cast<double>(__uint_as_float(m)) * r.rstd) : 0;
-      s = m > 0 ? __int_as_float((e + 127) << 23) : 1.f;
-      const float inv = ldexpf(1.f, -e);
+      const int e = m > 0.f ? e4m3_scale_bits(m, r.factor, r.rstd) : 127;
+      s = __int_as_float(e << 23);
+      const float inv = __int_as_float((254 - e) << 23);
+      const float2 f = make_float2(r.factor * inv, r.factor * inv), g = make_float2(r.rest * inv, r.rest * inv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = zw[i] * r.factor * inv;
+      for (int i = 0; i < 4; ++i) y[i] = fma2(zw[i], f, mul2(zw[i], g));
     }
-    static_cast<uint2*>(p.out)[at] = make_uint2(codes_e4m3(y), codes_e4m3(y + 4));
+    const float* yv = reinterpret_cast<const float*>(y);
+    static_cast<uint2*>(p.out)[at] = make_uint2(codes_e4m3(yv), codes_e4m3(yv + 4));
     if ((threadIdx.x & 15) == 0) p.scale[at >> 4] = s;
   } else {
-    uint32_t q[2] = {0u, 0u};
-    if (!r.bad) {
+    uint32_t c[8];
+    if (!r.wide) {
+      // (NaN and infinite products are in rows whose factor is 0 and whose codes are cleared below)
+      const float2 f = make_float2(r.factor, r.factor), magic = make_float2(12582912.f, 12582912.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = r.wide ? __double2int_rn(static_cast<double>(zw[i]) * r.factor_wide) : __float2int_rn(zw[i] * r.factor);
-        q[i >> 2] |= (static_cast<uint32_t>(c) & 0xffu) << (8 * (i & 3));
+      for (int i = 0; i < 4; ++i) {
+        const float2 y = fma2(zw[i], f, magic);
+        c[2 * i] = __float_as_uint(y.x);
+        c[2 * i + 1] = __float_as_uint(y.y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[2 * i] = static_cast<uint32_t>(__double2int_rn(static_cast<double>(zw[i].x) * r.factor_wide));
+        c[2 * i + 1] = static_cast<uint32_t>(__double2int_rn(static_cast<double>(zw[i].y) * r.factor_wide));
       }
     }
-    static_cast<uint2*>(p.out)[at] = make_uint2(q[0], q[1]);
-  }
-}
-
-// z of vector v of a row (and its store); `again`: the second pass of a long row, where
-// the sum was stored already (over the residual, it may be) and is read back.
-MOE_DEVINL void load_z(const NormParams& p, long long at, float (&z)[8], bool again) {
-  if (again && p.res_out != nullptr) {
-    unpack8(p.res_out[at], z);
-    return;
-  }
-  unpack8(p.x[at], z);
-  if (p.res != nullptr) {
-    float r[8];
-    unpack8(p.res[at], r);
+    uint32_t q[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] += r[i];
-    const uint4 packed = pack8(z);
-    if (p.res_out != nullptr) p.res_out[at] = packed;
-    unpack8(packed, z);
+    for (int i = 0; i < 2; ++i)
+      q[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
+    static_cast<uint2*>(p.out)[at] = r.bad ? make_uint2(0u, 0u) : make_uint2(q[0], q[1]);
   }
 }
 
-// One block per row.  VPT > 0: thread t holds vectors t, t + blockDim, ... (VPT of them) in
-// registers; VPT == 0 (rows of more than 32768 channels): two passes over the row.
+// The products zw of a vector z with its weights; adds its squares to ss, its largest to amax.
+template <int FMT>
+MOE_DEVINL void products(uint4 zq, uint4 wq, float2 (&zw)[4], double& ss, float& amax) {
+  const uint32_t z[4] = {zq.x, zq.y, zq.z, zq.w}, w[4] = {wq.x, wq.y, wq.z, wq.w};
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack2(z[i]);
+    s = fma2(v, v, s);
+    zw[i] = mul2(v, unpack2(w[i]));
+    if (FMT == NORM_INT8) amax = max_abs(max_abs(amax, zw[i].x), zw[i].y);
+  }
+  ss += static_cast<double>(s.x + s.y);
+}
+
+// Rows of at most 8 * VPT * blockDim channels, one at a time per block.  Thread t holds vectors
+// t, t + blockDim, ... (VPT of them).  Shared memory: two buffers of [x, residual][VPT][blockDim]
+// vectors, each thread's own.
 template <int FMT, int VPT>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(1024) norm_rows_kernel(const NormParams p, const int T) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ double sh_ss[1][32];
-  __shared__ uint32_t sh_amax[1][32];
-  const long long row = blockIdx.x;
-  const long long base = row * p.nvec;
-  double ss = 0.0;
-  uint32_t amax = 0;
-  constexpr int HELD = VPT > 0 ? VPT : 1;
-  float zw[HELD][8];
-  auto take = [&](int v, float (&o)[8]) {
-    float z[8], w[8];
-    load_z(p, base + v, z, false);
-    unpack8(__ldg(p.w + v), w);
-    float s = 0.f;
+  extern __shared__ uint4 buf[];
+  __shared__ double sh_ss[2][32];
+  __shared__ uint32_t sh_amax[2][32];
+  const int nt = blockDim.x, tid = threadIdx.x;
+  const int streams = p.res != nullptr ? 2 : 1;
+  auto slot = [&](int b, int stream, int i) { return buf + ((b * streams + stream) * VPT + i) * nt + tid; };
+  auto fetch = [&](long long row, int b) {
+    if (row < T) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s = fmaf(z[i], z[i], s);
-      o[i] = z[i] * w[i];
-      if (FMT == NORM_INT8) amax = max(amax, abs_bits(o[i]));
+      for (int i = 0; i < VPT; ++i) {
+        const int v = tid + i * nt;
+        if (v < p.nvec) {
+          cp_async16(slot(b, 0, i), p.x + row * p.nvec + v);
+          if (streams == 2) cp_async16(slot(b, 1, i), p.res + row * p.nvec + v);
+        }
+      }
     }
-    ss += static_cast<double>(s);
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if constexpr (VPT > 0) {
+  constexpr bool HOLD_W = VPT <= 2;  // (four vectors of weights do not fit the registers beside zw)
+  uint4 w[HOLD_W ? VPT : 1];
+  long long row = blockIdx.x;
+  fetch(row, 0);
+  if constexpr (HOLD_W) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < p.nvec) take(v, zw[i]);
-    }
-  } else {
-    for (int v = threadIdx.x; v < p.nvec; v += blockDim.x) take(v, zw[0]);
+    for (int i = 0; i < VPT; ++i) w[i] = tid + i * nt < p.nvec ? __ldg(p.w + tid + i * nt) : make_uint4(0, 0, 0, 0);
   }
-  block_reduce(ss, amax, sh_ss, sh_amax, 0);
-  const RowScale r = row_scale<FMT>(ss, amax, p, row);
-  if constexpr (VPT > 0) {
+  for (int b = 0; row < T; row += gridDim.x, b ^= 1) {
+    fetch(row + gridDim.x, b ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    double ss = 0.0;
+    float amax = 0.f;
+    float2 zw[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
+      const int v = tid + i * nt;
+      if (v < p.nvec) {
+        uint4 z = *slot(b, 0, i);
+        if (streams == 2) {
+          z = add8(z, *slot(b, 1, i));
+          if (p.res_out != nullptr) p.res_out[row * p.nvec + v] = z;
+        }
+        if constexpr (HOLD_W) products<FMT>(z, w[i], zw[i], ss, amax);
+        else products<FMT>(z, __ldg(p.w + v), zw[i], ss, amax);
+      }
+    }
+    uint32_t amax_bits = __float_as_uint(amax);
+    block_reduce(ss, amax_bits, sh_ss, sh_amax, b);
+    const RowScale r = row_scale<FMT>(ss, amax_bits, p, row);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = tid + i * nt;
       if (v < p.nvec) store_vec<FMT>(zw[i], r, p, row, v);
     }
-  } else {
-    for (int v = threadIdx.x; v < p.nvec; v += blockDim.x) {
-      float z[8], w[8], o[8];
-      load_z(p, base + v, z, true);
-      unpack8(__ldg(p.w + v), w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = z[i] * w[i];
-      store_vec<FMT>(o, r, p, row, v);
-    }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Longer rows: two passes, a block per row.  The second reads the sum back where it was stored
+// (over the residual, it may be) and makes it again where it was not.
+template <int FMT>
+__global__ void __launch_bounds__(1024) norm_long_kernel(const NormParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ double sh_ss[2][32];
+  __shared__ uint32_t sh_amax[2][32];
+  const long long row = blockIdx.x, base = row * p.nvec;
+  double ss = 0.0;
+  float amax = 0.f;
+  float2 zw[4];
+  for (int v = threadIdx.x; v < p.nvec; v += blockDim.x) {
+    uint4 z = p.x[base + v];
+    if (p.res != nullptr) {
+      z = add8(z, p.res[base + v]);
+      if (p.res_out != nullptr) p.res_out[base + v] = z;
+    }
+    products<FMT>(z, __ldg(p.w + v), zw, ss, amax);
+  }
+  uint32_t amax_bits = __float_as_uint(amax);
+  block_reduce(ss, amax_bits, sh_ss, sh_amax, 0);
+  const RowScale r = row_scale<FMT>(ss, amax_bits, p, row);
+  for (int v = threadIdx.x; v < p.nvec; v += blockDim.x) {
+    uint4 z;
+    if (p.res_out != nullptr) z = p.res_out[base + v];
+    else z = p.res != nullptr ? add8(p.x[base + v], p.res[base + v]) : p.x[base + v];
+    products<FMT>(z, __ldg(p.w + v), zw, ss, amax);
+    store_vec<FMT>(zw, r, p, row, v);
+  }
+}
+
+template <int FMT, int VPT>
+cudaError_t launch_rows(const NormParams& p, int T, cudaStream_t st) {
+  const int threads = 32 * ((p.nvec + 32 * VPT - 1) / (32 * VPT));
+  const int smem = 2 * (p.res != nullptr ? 2 : 1) * VPT * threads * 16;
+  auto kern = norm_rows_kernel<FMT, VPT>;
+  if (smem > 40 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+  }
+  // blocks per SM: by shared memory, by threads (1536 leave 42 registers each), 16 at most
+  int per_sm = 227 * 1024 / (smem + 2048);
+  per_sm = per_sm < 1536 / threads ? per_sm : 1536 / threads;
+  per_sm = per_sm < 1 ? 1 : (per_sm > 16 ? 16 : per_sm);
+  const long long most = static_cast<long long>(num_sms()) * per_sm;
+  const int grid = static_cast<int>(T < most ? T : most);
+  return launch_k(kern, grid, threads, smem, st, p, T);
 }
 
 template <int FMT>
 cudaError_t launch_fmt(const NormParams& p, int T, cudaStream_t st) {
-  // threads: whole warps, as few as hold the row at VPT vectors each
-  const int warps = (p.nvec + 31) / 32;
-  auto threads = [&](int vpt) { return 32 * ((warps + vpt - 1) / vpt); };
-  if (p.nvec <= 1024 && T <= 4 * num_sms()) return launch_k(norm_kernel<FMT, 1>, T, threads(1), 0, st, p);
-  if (p.nvec <= 4096) return launch_k(norm_kernel<FMT, 4>, T, threads(4), 0, st, p);
-  return launch_k(norm_kernel<FMT, 0>, T, 1024, 0, st, p);
+  if (p.nvec <= 1024 && T <= num_sms()) return launch_rows<FMT, 1>(p, T, st);
+  if (p.nvec <= 2048) return launch_rows<FMT, 2>(p, T, st);
+  if (p.nvec <= 3328) return launch_rows<FMT, 4>(p, T, st);
+  return launch_k(norm_long_kernel<FMT>, T, 1024, 0, st, p);
 }
 
 }  // namespace

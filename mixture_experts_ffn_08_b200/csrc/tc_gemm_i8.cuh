@@ -182,6 +182,34 @@ MOE_DEVINL void i8_store32(const I8Params& p, long long row, int col, const floa
   }
 }
 
+MOE_DEVINL void i8_store1(const I8Params& p, long long row, int col, float v) {
+  const long long at = row * p.ldo + col;
+  if (p.out_type == MOE_OUT_FP32) static_cast<float*>(p.out)[at] = v;
+  else if (p.out_type == MOE_OUT_BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p.out)[at] = __float2half_rn(v);
+}
+
+MOE_DEVINL void i8_store4(const I8Params& p, long long row, int col, const float (&v)[4], int n) {
+  const long long at = row * p.ldo + col;
+  if (n >= 4 && p.out_type == MOE_OUT_FP32 && (reinterpret_cast<uintptr_t>(static_cast<float*>(p.out) + at) & 15) == 0) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+  } else if (n >= 4 && p.out_type != MOE_OUT_FP32 &&
+             (reinterpret_cast<uintptr_t>(static_cast<uint16_t*>(p.out) + at) & 7) == 0) {
+    uint2 w;
+    if (p.out_type == MOE_OUT_BF16) {
+      w = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else {
+      const __half2 lo = __floats2half2_rn(v[0], v[1]), hi = __floats2half2_rn(v[2], v[3]);
+      w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) i8_store1(p, row, col + i, v[i]);
+  }
+}
+
 // ---- output boxes: 32 rows x 128 bytes, 128-byte swizzle (16-byte piece j of row r at j ^ (r & 7))
 // Direct stores of a lane's own row touch 32 lines per instruction; measured on B200 they cost
 // the 8192 x 14336 x 4096 product 16 of 345 us and the 128-expert prefill 300 of 2690 us, where
@@ -478,6 +506,250 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     __syncwarp();
     if constexpr (PAIR) tmem_dealloc_pair(tmem_base, Cfg::TMEM_COLS);
     else tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------------- few rows
+// The dense product where its tiles do not fill the SMs: KS CTAs of a cluster share one
+// 128 x BN tile, each over its part of K.  Each leaves its s32 accumulator in its own shared
+// memory (the stage ring, which is done by then); after a cluster barrier CTA r adds the KS parts
+// of its BN / KS columns over distributed shared memory, in the order of the parts (any order
+// gives the same integer), scales and stores them.  No workspace, no atomics, one launch.
+template <int BN_, int STAGES_>
+struct I8SplitCfg {
+  static constexpr int BN = BN_;
+  static constexpr int STAGES = STAGES_;
+  static constexpr int BK = 128;
+  static constexpr int A_BYTES = 128 * BK;
+  static constexpr int STAGE_BYTES = A_BYTES + BN * BK;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+  static constexpr int TMEM_COLS = BN;
+  static constexpr int THREADS = 192;
+  static_assert(128 * BN * 4 <= STAGES * STAGE_BYTES, "the accumulator fits the ring");
+  static_assert(SMEM_BYTES + 2048 <= 227 * 1024, "shared memory");
+};
+
+MOE_DEVINL int4 ld_cluster_int4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Grid: (KS, N-tiles, M-tiles), clusters of KS.
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+    tc_gemm_i8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                            const int a_box, const I8Params p) {
+  constexpr int BN = Cfg::BN, BK = Cfg::BK, STAGES = Cfg::STAGES;
+  constexpr uint32_t IDESC = idesc_i8_s32(128, BN);
+  extern __shared__ uint8_t dsmem[];
+  __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES], done_bar;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ volatile int abort_flag;
+
+  const int warp = warp_id(), lane = lane_id();
+  const uint32_t pad = (1024u - (smem_u32(dsmem) & 1023u)) & 1023u;
+  uint8_t* smem = dsmem + pad;
+  const int ks = gridDim.x, part = blockIdx.x;  // the cluster spans the grid's x
+  const int KB = (p.K + BK - 1) / BK;
+  int kb0, kb1;
+  k_slice(part, ks, KB, kb0, kb1);
+  const int m0 = blockIdx.z * 128, col0 = blockIdx.y * BN;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    mbar_init(&done_bar, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_base_sh, Cfg::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_sh;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      int issued = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait_bounded(&empty_bar[s], ph ^ 1u, &abort_flag)) break;
+        uint8_t* sa = smem + s * Cfg::STAGE_BYTES;
+        mbar_arrive_expect_tx(&full_bar[s], static_cast<uint32_t>((a_box + BN) * BK));
+        tma_load_2d(sa, &tmA, kb * BK, m0, &full_bar[s]);
+        tma_load_2d(sa + Cfg::A_BYTES, &tmB, kb * BK, col0, &full_bar[s]);
+        ++issued;
+        if (++s == STAGES) { s = 0; ph ^= 1u; }
+      }
+      volatile int no_abort = 0;
+      const int back = issued < STAGES ? issued : STAGES;
+      for (int j = 0; j < back; ++j) {
+        if (s == 0) { s = STAGES - 1; ph ^= 1u; } else { --s; }
+        mbar_wait_bounded(&full_bar[s], ph, &no_abort);
+      }
+      if (no_abort) abort_flag = 1;
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait_bounded(&full_bar[s], ph, &abort_flag)) break;
+        tc_fence_after();
+        const uint32_t a0 = smem_u32(smem + s * Cfg::STAGE_BYTES);
+        const uint32_t b0 = a0 + Cfg::A_BYTES;
+#pragma unroll
+        for (int k = 0; k < BK / 32; ++k)
+          umma_i8<1>(tmem_base, smem_desc_sw128(a0 + k * 32), smem_desc_sw128(b0 + k * 32), IDESC, kb != kb0 || k != 0);
+        umma_commit(&empty_bar[s]);
+        if (++s == STAGES) { s = 0; ph ^= 1u; }
+      }
+      umma_commit(&done_bar);
+      volatile int no_abort = 0;
+      mbar_wait_bounded(&done_bar, 0, &no_abort);
+      if (no_abort) abort_flag = 1;
+    }
+  }
+  // the products and the copies are done (or were given up): TMEM may be read, the ring written
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int q = warp & 3;
+  const int row = q * 32 + lane;
+  const bool row_ok = m0 + row < p.dense_rows;
+  const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+  if (ks == 1) {
+    if (warp >= 2) {
+      const float sa = row_ok ? __ldg(p.a_scale + m0 + row) : 0.f;
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tbase + c, r);
+        tmem_ld_wait(r);
+        if (!row_ok || col0 + c >= p.N) continue;
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int n = col0 + c + i;
+          const float sw = n < p.N ? __ldg(p.w_scale + n) : 0.f;
+          const float b = n < p.N && p.bias != nullptr ? __ldg(p.bias + n) : 0.f;
+          v[i] = fmaf(__int2float_rn(static_cast<int>(r[i])), sa * sw, b);
+        }
+        i8_store32(p, m0 + row, col0 + c, v, p.N - col0 - c);
+      }
+    }
+  } else {
+    // parts as [column group of 4][row] int4: 512 contiguous bytes per warp and access
+    if (warp >= 2) {
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tbase + c, r);
+        tmem_ld_wait(r);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<int4*>(smem + ((((c + i) >> 2) * 128 + row) << 4)) =
+              make_int4(static_cast<int>(r[i]), static_cast<int>(r[i + 1]), static_cast<int>(r[i + 2]),
+                        static_cast<int>(r[i + 3]));
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+    const int cols = BN / ks;  // columns that this CTA finishes: a multiple of 4
+    if (warp >= 2 && row_ok) {
+      const float sa = __ldg(p.a_scale + m0 + row);
+      const uint32_t mine = smem_u32(smem) + row * 16;
+      for (int c = part * cols; c < (part + 1) * cols && col0 + c < p.N; c += 4) {
+        int4 t = make_int4(0, 0, 0, 0);
+        for (int k = 0; k < ks; ++k) {
+          const int4 v = ld_cluster_int4(mapa_shared(mine + (c >> 2) * 2048, k));
+          t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+        }
+        const int a[4] = {t.x, t.y, t.z, t.w};
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = col0 + c + i;
+          const float sw = n < p.N ? __ldg(p.w_scale + n) : 0.f;
+          const float b = n < p.N && p.bias != nullptr ? __ldg(p.bias + n) : 0.f;
+          v[i] = fmaf(__int2float_rn(a[i]), sa * sw, b);
+        }
+        i8_store4(p, m0 + row, col0 + c, v, p.N - col0 - c);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // the others have read this CTA's part
+  }
+  __syncthreads();
+  if (abort_flag && threadIdx.x == 0) set_status(p.status, MOE_DEV_TIMEOUT);
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+  }
+}
+
+// One to four rows: nothing to share in a tile, the weights are read once whatever is done with
+// them.  A warp per output channel, 16 codes per lane and load, integer dot products; the few
+// rows of A come from L1.  UNROLL loads of weights are in flight per lane.
+template <int M>
+__global__ void __launch_bounds__(256) i8_gemv_kernel(const int8_t* __restrict__ a, int64_t lda,
+                                                      const int8_t* __restrict__ w, int64_t ldw, const I8Params p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int UNROLL = M == 1 ? 8 : 4;
+  const int lane = lane_id();
+  const int n = blockIdx.x * 8 + warp_id();
+  if (n >= p.N) return;  // warp-uniform
+  const int nvec = p.K / 16;
+  const int4* wr = reinterpret_cast<const int4*>(w + n * ldw);
+  int acc[M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) acc[m] = 0;
+  for (int v0 = lane; v0 < nvec; v0 += 32 * UNROLL) {
+    int4 q[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+      q[u] = v0 + 32 * u < nvec ? __ldcs(wr + v0 + 32 * u) : make_int4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int v = v0 + 32 * u < nvec ? v0 + 32 * u : lane;  // (past the end: times 0)
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const int4 x = __ldg(reinterpret_cast<const int4*>(a + m * lda) + v);
+        acc[m] = __dp4a(q[u].x, x.x, acc[m]);
+        acc[m] = __dp4a(q[u].y, x.y, acc[m]);
+        acc[m] = __dp4a(q[u].z, x.z, acc[m]);
+        acc[m] = __dp4a(q[u].w, x.w, acc[m]);
+      }
+    }
+  }
+  float mine = 0.f;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const int t = __reduce_add_sync(0xffffffffu, acc[m]);
+    if (lane == m) mine = __int2float_rn(t);
+  }
+  if (lane < M) {
+    const float v = fmaf(mine, __ldg(p.a_scale + lane) * __ldg(p.w_scale + n), p.bias != nullptr ? __ldg(p.bias + n) : 0.f);
+    i8_store1(p, lane, n, v);
   }
 }
 

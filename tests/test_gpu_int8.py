@@ -64,6 +64,17 @@ def test_linear_large(M, N, K, dtype):
     check_linear(args, ref, tol)
 
 
+@pytest.mark.parametrize("M,N,K", [(8, 4096, 7168), (16, 64, 4096), (33, 40, 2048), (128, 300, 8192), (20, 1000, 512),
+                                   (300, 2304, 384), (600, 1500, 2048), (5, 16, 16), (100, 4700, 640), (30, 4700, 640),
+                                   (64, 2300, 1008), (128, 7168, 4096), (1, 5, 16), (4, 1000, 9008), (2, 333, 4112)])
+@pytest.mark.parametrize("dtype", list(KIND))
+def test_linear_few_rows(M, N, K, dtype):
+    """One round of tiles: every width, one to eight parts of K, odd ends; and the one-row forms."""
+    args, ref, tol = linear_case(M, N, K, dtype, pad=(16, 16, 0 if dtype == torch.float16 else 1), seed=M)
+    linear(*args)
+    check_linear(args, ref, tol)
+
+
 @pytest.mark.parametrize("M", [1, 3, 20, 200])
 def test_linear_longest_sum(M):
     """K = 131056 with every code -128: the sum 2147221504 is the largest that 32 bits hold here."""
