@@ -18,6 +18,7 @@ from . import workloads as W
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_b200.so")
 _lib = None
+_gpu_seen = False
 
 MOE_OK = 0
 MOE_DEV_BAD_EXPERT_ID = 0x1
@@ -100,7 +101,9 @@ EXPORTED = sorted(_SIGS)
 
 def lib(require_gpu: bool = True):
     """The loaded CUDA library.  Raises if it is not built or (by default) no GPU."""
-    global _lib
+    global _lib, _gpu_seen
+    if _lib is not None and _gpu_seen:  # (asking torch for the GPU takes longer than a launch)
+        return _lib
     if _lib is None:
         if not os.path.exists(_LIB_PATH):
             raise MoEError(f"CUDA library not built: {_LIB_PATH} (run "
@@ -111,8 +114,10 @@ def lib(require_gpu: bool = True):
             f.restype = res
             f.argtypes = args
         _lib = l
-    if require_gpu and not torch.cuda.is_available():
-        raise MoEError("no CUDA device: the MoE layer runs only in its CUDA kernels")
+    if require_gpu:
+        if not torch.cuda.is_available():
+            raise MoEError("no CUDA device: the MoE layer runs only in its CUDA kernels")
+        _gpu_seen = True
     return _lib
 
 
@@ -124,8 +129,16 @@ def _ptr(t):
     return int(t)
 
 
+# The current stream's handle without the Stream object around it, which takes 3 us to make,
+# as long as a launch; where this torch has no such call, the object it is.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(s):
     if s is None:
+        if _raw_stream is not None:
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, torch.cuda.Stream):
         return s.cuda_stream

@@ -132,10 +132,10 @@ cudaError_t launch_i8_split(const void* a, int64_t lda, const void* w, int64_t l
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-template <int M>
+template <int M, int R>
 cudaError_t launch_i8_gemv(const void* a, int64_t lda, const void* w, int64_t ldw, const I8Params& p, cudaStream_t st) {
   trace_before(MOE_K_LINEAR, st);
-  const cudaError_t err = launch_k(i8_gemv_kernel<M>, static_cast<int>(cdiv(p.N, 8)), 256, 0, st,
+  const cudaError_t err = launch_k(i8_gemv_kernel<M, R>, static_cast<int>(cdiv(p.N, 8 * R)), 256, 0, st,
                                    static_cast<const int8_t*>(a), lda, static_cast<const int8_t*>(w), ldw, p);
   trace_after(MOE_K_LINEAR, st);
   return err != cudaSuccess ? err : cudaGetLastError();
@@ -306,14 +306,16 @@ cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, cons
   p.out_type = out_type;
   p.ldo = ldo;
   p.status = status;
-  switch (M) {
-    case 1: return launch_i8_gemv<1>(a, lda, w, ldw, p, st);
-    case 2: return launch_i8_gemv<2>(a, lda, w, ldw, p, st);
-    case 3: return launch_i8_gemv<3>(a, lda, w, ldw, p, st);
-    case 4: return launch_i8_gemv<4>(a, lda, w, ldw, p, st);
-    default: break;
-  }
   const long long sms = num_sms();
+  // One row, or two, or three and four of few channels (those read each row of A once per
+  // channel): dot products.  Measured: 2 x 4096 x 7168 8.0 us against 10.0 with the tensor cores,
+  // 4 x 512 x 4096 3.3 against 5.4, but 4 x 4096 x 7168 10.8 against 10.0.  Two channels per warp
+  // where that still leaves every SM eight warps of four: 2 x 14336 x 4096 13.6 against 16.5 us.
+  if (M == 1) return launch_i8_gemv<1, 1>(a, lda, w, ldw, p, st);
+  if (M == 2 && N >= 64 * sms) return launch_i8_gemv<2, 2>(a, lda, w, ldw, p, st);
+  if (M == 2) return launch_i8_gemv<2, 1>(a, lda, w, ldw, p, st);
+  if (M == 3 && N < 16 * sms) return launch_i8_gemv<3, 1>(a, lda, w, ldw, p, st);
+  if (M == 4 && N < 16 * sms) return launch_i8_gemv<4, 1>(a, lda, w, ldw, p, st);
   const long long mt = cdiv(M, 128), pairs = cdiv(M, 256) * cdiv(N, 256);
   // pair tiles where they fill the SMs
   if (pairs >= sms / 2)
@@ -322,23 +324,27 @@ cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, cons
   if (mt * cdiv(N, 128) > sms)
     return launch_i8<I8Cfg<1, 128, false, 6>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 128), MOE_K_LINEAR, st);
   // One round of tiles of 128 x bn over ks parts of K each: of those that fit, the one whose CTAs
-  // load the fewest operand bytes; exchanging the parts counts as 32 KB per CTA.
+  // load the fewest operand bytes.  Exchanging the parts takes about as long as loading 300 KB does
+  // for 128 x 128 sums, and less for fewer (measured, in four parts and in one: 128 x 4096 x 1024
+  // 8.0 and 5.1 us, 128 x 4096 x 7168 13.4 and 19.9, 8 x 512 x 4096 5.4 and 11.8, 77 x 1031 x 1552
+  // 5.6 and 7.4).
   const int KB = static_cast<int>(cdiv(K, 128)), box = M <= kI8SmallRows ? kI8SmallRows : 128;
   int best_bn = 128, best_ks = 1;
   long long best = -1;
   for (int bn = 32; bn <= 128; bn *= 2)
-    for (int ks = 1; ks <= 8 && ks * 2 <= KB + 1; ks *= 2) {
+    for (int ks = 1; ks <= 4 && ks * 2 <= KB + 1; ks *= 2) {
       if (mt * cdiv(N, bn) * ks > sms) continue;
-      const long long cost = static_cast<long long>(box + bn) * 128 * cdiv(KB, ks) + (ks > 1 ? 32768 : 0);
+      const long long cost = static_cast<long long>(box + bn) * 128 * cdiv(KB, ks) +
+                             (ks > 1 ? (40 << 10) + bn * box * 16LL : 0);
       if (best < 0 || cost < best) {
         best = cost;
         best_bn = bn;
         best_ks = ks;
       }
     }
-  if (best_bn == 32) return launch_i8_split<I8SplitCfg<32, 10>>(a, lda, w, ldw, p, best_ks, st);
-  if (best_bn == 64) return launch_i8_split<I8SplitCfg<64, 8>>(a, lda, w, ldw, p, best_ks, st);
-  return launch_i8_split<I8SplitCfg<128, 6>>(a, lda, w, ldw, p, best_ks, st);
+  if (best_bn == 32) return launch_i8_split<I8SplitCfg<32, 9>>(a, lda, w, ldw, p, best_ks, st);
+  if (best_bn == 64) return launch_i8_split<I8SplitCfg<64, 7>>(a, lda, w, ldw, p, best_ks, st);
+  return launch_i8_split<I8SplitCfg<128, 4>>(a, lda, w, ldw, p, best_ks, st);
 }
 
 }  // namespace moe

@@ -511,10 +511,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 
 // ---------------------------------------------------------------------------------- few rows
 // The dense product where its tiles do not fill the SMs: KS CTAs of a cluster share one
-// 128 x BN tile, each over its part of K.  Each leaves its s32 accumulator in its own shared
-// memory (the stage ring, which is done by then); after a cluster barrier CTA r adds the KS parts
-// of its BN / KS columns over distributed shared memory, in the order of the parts (any order
-// gives the same integer), scales and stores them.  No workspace, no atomics, one launch.
+// 128 x BN tile, each over its part of K.  A CTA finishes BN / KS of the columns: the others push
+// their s32 sums of those columns into its shared memory (posted stores, nothing waits for a
+// round trip), and after one cluster barrier it adds the KS parts (any order gives the same
+// integer), scales and stores them.  No workspace, no atomics, one launch.
+// Measured on B200, 128 x 7168 x 4096: reading the parts from the peers instead of having them
+// pushed cost 5 us more.
 template <int BN_, int STAGES_>
 struct I8SplitCfg {
   static constexpr int BN = BN_;
@@ -522,20 +524,18 @@ struct I8SplitCfg {
   static constexpr int BK = 128;
   static constexpr int A_BYTES = 128 * BK;
   static constexpr int STAGE_BYTES = A_BYTES + BN * BK;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+  // received parts: [part][column group of 4][row] int4, 512 contiguous bytes per warp and access
+  static constexpr int PART_BYTES = 128 * BN * 4;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + PART_BYTES + 1024;
   static constexpr int TMEM_COLS = BN;
   static constexpr int THREADS = 192;
-  static_assert(128 * BN * 4 <= STAGES * STAGE_BYTES, "the accumulator fits the ring");
-  static_assert(SMEM_BYTES + 2048 <= 227 * 1024, "shared memory");
+  static_assert(SMEM_BYTES + 2 * BN * 4 + 1024 <= 227 * 1024, "shared memory");
 };
 
-MOE_DEVINL int4 ld_cluster_int4(uint32_t addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
+MOE_DEVINL void st_cluster_v4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
                : "memory");
-  return v;
 }
 
 // Grid: (KS, N-tiles, M-tiles), clusters of KS.
@@ -547,12 +547,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   constexpr uint32_t IDESC = idesc_i8_s32(128, BN);
   extern __shared__ uint8_t dsmem[];
   __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES], done_bar;
+  __shared__ float scale_sh[BN], bias_sh[BN];
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_flag;
 
   const int warp = warp_id(), lane = lane_id();
   const uint32_t pad = (1024u - (smem_u32(dsmem) & 1023u)) & 1023u;
   uint8_t* smem = dsmem + pad;
+  uint8_t* parts = smem + STAGES * Cfg::STAGE_BYTES;
   const int ks = gridDim.x, part = blockIdx.x;  // the cluster spans the grid's x
   const int KB = (p.K + BK - 1) / BK;
   int kb0, kb1;
@@ -580,6 +582,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_sh;
+  // (a CTA's shared memory may be written once it runs: waited for before the first push)
+  if (ks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_launch_dependents();
   pdl_wait();
 
@@ -626,17 +630,24 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       if (no_abort) abort_flag = 1;
     }
   }
-  // the products and the copies are done (or were given up): TMEM may be read, the ring written
+  if (warp >= 2) {
+    for (int c = threadIdx.x - 64; c < BN; c += 128) {
+      const bool in = col0 + c < p.N;
+      scale_sh[c] = in ? __ldg(p.w_scale + col0 + c) : 0.f;
+      bias_sh[c] = in && p.bias != nullptr ? __ldg(p.bias + col0 + c) : 0.f;
+    }
+  }
+  // the products and the copies are done, or were given up
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const int q = warp & 3;
   const int row = q * 32 + lane;
-  const bool row_ok = m0 + row < p.dense_rows;
   const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
   if (ks == 1) {
-    if (warp >= 2) {
+    const bool row_ok = m0 + row < p.dense_rows;
+    if (warp >= 2 && m0 + q * 32 < p.dense_rows) {
       const float sa = row_ok ? __ldg(p.a_scale + m0 + row) : 0.f;
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
@@ -646,56 +657,51 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         if (!row_ok || col0 + c >= p.N) continue;
         float v[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int n = col0 + c + i;
-          const float sw = n < p.N ? __ldg(p.w_scale + n) : 0.f;
-          const float b = n < p.N && p.bias != nullptr ? __ldg(p.bias + n) : 0.f;
-          v[i] = fmaf(__int2float_rn(static_cast<int>(r[i])), sa * sw, b);
-        }
+        for (int i = 0; i < 32; ++i)
+          v[i] = fmaf(__int2float_rn(static_cast<int>(r[i])), sa * scale_sh[c + i], bias_sh[c + i]);
         i8_store32(p, m0 + row, col0 + c, v, p.N - col0 - c);
       }
     }
   } else {
-    // parts as [column group of 4][row] int4: 512 contiguous bytes per warp and access
-    if (warp >= 2) {
+    const int log_cols = 31 - __clz(BN / ks), cols = 1 << log_cols;  // columns that a CTA finishes, 8 at least
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (warp >= 2 && m0 + q * 32 < p.dense_rows) {
+      const uint32_t mine = smem_u32(parts) + part * (cols * 512) + row * 16;
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(tbase + c, r);
         tmem_ld_wait(r);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4)
-          *reinterpret_cast<int4*>(smem + ((((c + i) >> 2) * 128 + row) << 4)) =
-              make_int4(static_cast<int>(r[i]), static_cast<int>(r[i + 1]), static_cast<int>(r[i + 2]),
-                        static_cast<int>(r[i + 3]));
+        for (int i = 0; i < 32; i += 4) {
+          const int owner = (c + i) >> log_cols;
+          st_cluster_v4(mapa_shared(mine + (((c + i) & (cols - 1)) >> 2) * 2048, owner), r + i);
+        }
       }
     }
     __syncwarp();
     cluster_sync();
-    const int cols = BN / ks;  // columns that this CTA finishes: a multiple of 4
-    if (warp >= 2 && row_ok) {
-      const float sa = __ldg(p.a_scale + m0 + row);
-      const uint32_t mine = smem_u32(smem) + row * 16;
-      for (int c = part * cols; c < (part + 1) * cols && col0 + c < p.N; c += 4) {
-        int4 t = make_int4(0, 0, 0, 0);
-        for (int k = 0; k < ks; ++k) {
-          const int4 v = ld_cluster_int4(mapa_shared(mine + (c >> 2) * 2048, k));
-          t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
-        }
-        const int a[4] = {t.x, t.y, t.z, t.w};
-        float v[4];
+    if (warp >= 2) {
+      // a thread per row, or four warps that share 32 rows' column groups
+      const bool narrow = a_box == kI8SmallRows;
+      const int r0 = narrow ? lane : row, step = narrow ? 4 : 1;
+      if (m0 + r0 < p.dense_rows) {
+        const float sa = __ldg(p.a_scale + m0 + r0);
+        for (int g = narrow ? q : 0; g < cols / 4; g += step) {
+          const int c = part * cols + 4 * g;
+          if (col0 + c >= p.N) break;
+          int t[4] = {0, 0, 0, 0};
+          for (int k = 0; k < ks; ++k) {
+            const int4 v = *reinterpret_cast<const int4*>(parts + k * (cols * 512) + g * 2048 + r0 * 16);
+            t[0] += v.x; t[1] += v.y; t[2] += v.z; t[3] += v.w;
+          }
+          float v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = col0 + c + i;
-          const float sw = n < p.N ? __ldg(p.w_scale + n) : 0.f;
-          const float b = n < p.N && p.bias != nullptr ? __ldg(p.bias + n) : 0.f;
-          v[i] = fmaf(__int2float_rn(a[i]), sa * sw, b);
+          for (int i = 0; i < 4; ++i) v[i] = fmaf(__int2float_rn(t[i]), sa * scale_sh[c + i], bias_sh[c + i]);
+          i8_store4(p, m0 + r0, col0 + c, v, p.N - col0 - c);
         }
-        i8_store4(p, m0 + row, col0 + c, v, p.N - col0 - c);
       }
     }
-    __syncwarp();
-    cluster_sync();  // the others have read this CTA's part
   }
   __syncthreads();
   if (abort_flag && threadIdx.x == 0) set_status(p.status, MOE_DEV_TIMEOUT);
@@ -706,51 +712,74 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   }
 }
 
+// 16 bytes read once (zero where !in); volatile, so that a batch of them is issued as a batch.
+MOE_DEVINL int4 ld_stream(const int4* p, bool in) {
+  int4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.cs.v4.s32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "l"(p), "r"(static_cast<int>(in)));
+  return v;
+}
+
 // One to four rows: nothing to share in a tile, the weights are read once whatever is done with
-// them.  A warp per output channel, 16 codes per lane and load, integer dot products; the few
-// rows of A come from L1.  UNROLL loads of weights are in flight per lane.
-template <int M>
+// them.  A warp per R output channels, 16 codes per lane and load, integer dot products; the few
+// rows of A come from L1, each load of them used for R channels.  R * UNROLL loads of weights are
+// in flight per lane.
+template <int M, int R>
 __global__ void __launch_bounds__(256) i8_gemv_kernel(const int8_t* __restrict__ a, int64_t lda,
                                                       const int8_t* __restrict__ w, int64_t ldw, const I8Params p) {
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int UNROLL = M == 1 ? 8 : 4;
+  constexpr int UNROLL = M == 1 ? 16 : 4;
   const int lane = lane_id();
-  const int n = blockIdx.x * 8 + warp_id();
-  if (n >= p.N) return;  // warp-uniform
+  const int n0 = (blockIdx.x * 8 + warp_id()) * R;
+  if (n0 >= p.N) return;  // warp-uniform
   const int nvec = p.K / 16;
-  const int4* wr = reinterpret_cast<const int4*>(w + n * ldw);
-  int acc[M];
+  int acc[R][M];
 #pragma unroll
-  for (int m = 0; m < M; ++m) acc[m] = 0;
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < M; ++m) acc[r][m] = 0;
   for (int v0 = lane; v0 < nvec; v0 += 32 * UNROLL) {
-    int4 q[UNROLL];
+    int4 q[R][UNROLL];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-      q[u] = v0 + 32 * u < nvec ? __ldcs(wr + v0 + 32 * u) : make_int4(0, 0, 0, 0);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u)
+        q[r][u] = ld_stream(reinterpret_cast<const int4*>(w + (n0 + r) * ldw) + v0 + 32 * u,
+                            v0 + 32 * u < nvec && (R == 1 || n0 + r < p.N));
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       const int v = v0 + 32 * u < nvec ? v0 + 32 * u : lane;  // (past the end: times 0)
 #pragma unroll
       for (int m = 0; m < M; ++m) {
         const int4 x = __ldg(reinterpret_cast<const int4*>(a + m * lda) + v);
-        acc[m] = __dp4a(q[u].x, x.x, acc[m]);
-        acc[m] = __dp4a(q[u].y, x.y, acc[m]);
-        acc[m] = __dp4a(q[u].z, x.z, acc[m]);
-        acc[m] = __dp4a(q[u].w, x.w, acc[m]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          acc[r][m] = __dp4a(q[r][u].x, x.x, acc[r][m]);
+          acc[r][m] = __dp4a(q[r][u].y, x.y, acc[r][m]);
+          acc[r][m] = __dp4a(q[r][u].z, x.z, acc[r][m]);
+          acc[r][m] = __dp4a(q[r][u].w, x.w, acc[r][m]);
+        }
       }
     }
   }
+  // lane r * M + m finishes channel r of row m
   float mine = 0.f;
 #pragma unroll
-  for (int m = 0; m < M; ++m) {
-    const int t = __reduce_add_sync(0xffffffffu, acc[m]);
-    if (lane == m) mine = __int2float_rn(t);
-  }
-  if (lane < M) {
-    const float v = fmaf(mine, __ldg(p.a_scale + lane) * __ldg(p.w_scale + n), p.bias != nullptr ? __ldg(p.bias + n) : 0.f);
-    i8_store1(p, lane, n, v);
-  }
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int t = __reduce_add_sync(0xffffffffu, acc[r][m]);
+      if (lane == r * M + m) mine = __int2float_rn(t);
+    }
+  const int n = n0 + lane / M, m = lane % M;
+  if (lane < R * M && n < p.N)
+    i8_store1(p, m, n, fmaf(mine, __ldg(p.a_scale + m) * __ldg(p.w_scale + n), p.bias != nullptr ? __ldg(p.bias + n) : 0.f));
 }
 
 }  // namespace moe
