@@ -234,6 +234,37 @@ MOE_DEVINL uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// Packed fp32 pairs.
+MOE_DEVINL float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return r;
+}
+MOE_DEVINL float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+        "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return r;
+}
+// max(a, |b|), NaN where either is.
+MOE_DEVINL float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+// v + 1.5 * 2^23 holds v rounded to the nearest whole number, ties to even, in its low bits
+// (|v| < 2^22): a multiply-add onto it makes an 8-bit code, whose byte low_bytes() collects.
+constexpr float kRoundMagic = 12582912.f;
+MOE_DEVINL uint32_t low_bytes(const uint32_t* c) {
+  return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+}
+
+MOE_DEVINL void cp_async16(void* dst_smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst_smem)), "l"(src) : "memory");
+}
+
 // Programmatic dependent launch.  Every kernel of the layer is launched so that the
 // next kernel in the stream may start while it runs (cudaLaunchAttribute
 // ProgrammaticStreamSerialization).  Each kernel first lets its dependents launch, then

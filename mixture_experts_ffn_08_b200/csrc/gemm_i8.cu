@@ -144,63 +144,156 @@ cudaError_t launch_i8_gemv(const void* a, int64_t lda, const void* w, int64_t ld
 // ------------------------------------------------------------------ h -> int8
 // q = rint(h / s), s = max|h| / 127 over the row (1 where the row is zero), as int8 codes and one
 // fp32 scale per row.  A row with a NaN or an infinity gets codes 0 and scale NaN, so that its
-// outputs are NaN.  Only the groups' real rows are read and written.  A warp per row, in two
-// passes: the row's largest value, then the codes.
-constexpr int kQuantWarps = 8;
+// outputs are NaN.  Only the groups' real rows are read and written.
+// What bounds it is HBM: 4 bytes read and 1 written per element.  A block holds one row in
+// registers between its largest value and its codes, up to 32 elements a thread, all of whose
+// loads are in flight at once; enough blocks share an SM that some load while others store.
+// (Fewer threads with more elements and the next row prefetched into shared memory took 346 us
+// for 131072 rows of 1536, and runs of rows per block instead of alternating ones 322, against
+// 170.)
+struct QuantParams {
+  const float* h;
+  const int32_t* offsets;
+  const int32_t* counts;
+  int E;
+  int cap;
+  int cols;
+  int8_t* codes;
+  float* scale;
+};
 
-MOE_DEVINL uint32_t quant4(float4 v, float f) {
-  return (static_cast<uint32_t>(__float2int_rn(v.x * f)) & 0xffu) |
-         (static_cast<uint32_t>(__float2int_rn(v.y * f)) & 0xffu) << 8 |
-         (static_cast<uint32_t>(__float2int_rn(v.z * f)) & 0xffu) << 16 |
-         (static_cast<uint32_t>(__float2int_rn(v.w * f)) & 0xffu) << 24;
-}
+// Numbers the real rows 0, 1, ... over the groups: pref[g] real rows lie before group g's.
+struct RealRows {
+  const QuantParams& p;
+  int* pref;  // [E + 1], shared
+  // one block-wide scan of the counts
+  MOE_DEVINL RealRows(const QuantParams& params, int* shared_pref, int* warp_tot) : p(params), pref(shared_pref) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int per = (p.E + blockDim.x - 1) / blockDim.x, g0 = tid * per;
+    int run = 0;
+    for (int g = g0; g < g0 + per && g < p.E; ++g) run += count(g);
+    int incl = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_tot[warp] = incl;
+    __syncthreads();
+    int acc = incl - run;
+    for (int w = 0; w < warp; ++w) acc += warp_tot[w];
+    for (int g = g0; g < g0 + per && g < p.E; ++g) {
+      pref[g] = acc;
+      acc += count(g);
+    }
+    if (warp == warps - 1 && lane == 31) pref[p.E] = acc;
+    __syncthreads();
+  }
+  MOE_DEVINL int count(int g) const {
+    return p.counts != nullptr ? __ldg(p.counts + g) : __ldg(p.offsets + g + 1) - __ldg(p.offsets + g);
+  }
+  MOE_DEVINL int total() const { return pref[p.E]; }
+  // where real row i lies
+  MOE_DEVINL long long row(int i) const {
+    int lo = 0, hi = p.E - 1;  // group with pref[g] <= i < pref[g+1]
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pref[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    return (p.cap > 0 ? static_cast<long long>(lo) * p.cap : __ldg(p.offsets + lo)) + i - pref[lo];
+  }
+};
 
 MOE_DEVINL uint32_t absmax4(uint32_t m, float4 v) {
-  m = max(m, __float_as_uint(v.x) & 0x7fffffffu);
-  m = max(m, __float_as_uint(v.y) & 0x7fffffffu);
-  m = max(m, __float_as_uint(v.z) & 0x7fffffffu);
-  return max(m, __float_as_uint(v.w) & 0x7fffffffu);
+  return __float_as_uint(max_abs(max_abs(max_abs(max_abs(__uint_as_float(m), v.x), v.y), v.z), v.w));
 }
 
-__global__ void __launch_bounds__(32 * kQuantWarps) quant_rows_kernel(
-    const float* __restrict__ h, const int32_t* __restrict__ offsets, const int32_t* __restrict__ counts, int E,
-    int cap, int cols, int8_t* __restrict__ codes, float* __restrict__ scale) {
+MOE_DEVINL uint32_t quant4(float4 v, float f) {
+  const float2 ff = make_float2(f, f), magic = make_float2(kRoundMagic, kRoundMagic);
+  const float2 a = fma2(make_float2(v.x, v.y), ff, magic), b = fma2(make_float2(v.z, v.w), ff, magic);
+  const uint32_t c[4] = {__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y)};
+  return low_bytes(c);
+}
+
+// Scale of a row whose largest value has bits m, and what its values are multiplied with.
+MOE_DEVINL float row_quant(uint32_t m, float& f, bool& bad) {
+  bad = m >= 0x7f800000u;
+  const float s = bad ? CUDART_NAN_F : (m == 0 ? 1.f : fmaxf(__uint_as_float(m) / 127.f, 1.1754943508222875e-38f));
+  f = bad ? 0.f : 1.f / s;
+  return s;
+}
+
+// The block's largest m, one barrier (`buf` alternates).
+MOE_DEVINL uint32_t block_max(uint32_t m, uint32_t (*sh)[32], int buf) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (warps == 1) return m;
+  if (lane == 0) sh[buf][threadIdx.x >> 5] = m;
+  __syncthreads();
+  return __reduce_max_sync(0xffffffffu, lane < warps ? sh[buf][lane] : 0u);
+}
+
+template <int VPT>
+__global__ void __launch_bounds__(512) quant_rows_kernel(const QuantParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int n4 = cols / 4;
-  const long long rows = cap > 0 ? static_cast<long long>(E) * cap : __ldg(offsets + E);
-  const long long warps = static_cast<long long>(gridDim.x) * kQuantWarps;
-  for (long long r = static_cast<long long>(blockIdx.x) * kQuantWarps + (threadIdx.x >> 5); r < rows; r += warps) {
-    if (counts != nullptr) {
-      int e;
-      long long first;
-      if (cap > 0) {
-        e = static_cast<int>(r / cap);
-        first = static_cast<long long>(e) * cap;
-      } else {
-        int lo = 0, hi = E - 1;  // smallest e with offsets[e+1] > r
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (__ldg(offsets + mid + 1) > r) hi = mid; else lo = mid + 1;
-        }
-        e = lo;
-        first = __ldg(offsets + e);
-      }
-      if (r - first >= __ldg(counts + e)) continue;
-    }
-    const float4* src = reinterpret_cast<const float4*>(h + r * cols);
+  __shared__ uint32_t sh[2][32];
+  __shared__ int pref[kI8MaxGroups + 1], warp_tot[32];
+  const int nt = blockDim.x, tid = threadIdx.x, n4 = p.cols / 4;
+  const RealRows rows(p, pref, warp_tot);
+  const int total = rows.total();
+  for (int k = blockIdx.x, turn = 0; k < total; k += gridDim.x, turn ^= 1) {
+    const long long r = rows.row(k);
+    const float4* src = reinterpret_cast<const float4*>(p.h + r * p.cols);
+    float4 x[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) x[i] = tid + i * nt < n4 ? __ldcs(src + tid + i * nt) : make_float4(0.f, 0.f, 0.f, 0.f);
     uint32_t m = 0;
-    for (int v = lane; v < n4; v += 32) m = absmax4(m, src[v]);
-    m = __reduce_max_sync(0xffffffffu, m);
-    const float amax = __uint_as_float(m);
-    const bool bad = m >= 0x7f800000u;
-    const float s = bad ? CUDART_NAN_F : (m == 0 ? 1.f : fmaxf(amax / 127.f, 1.1754943508222875e-38f));
-    const float f = bad ? 0.f : 1.f / s;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(codes + r * cols);
-    for (int v = lane; v < n4; v += 32) dst[v] = bad ? 0u : quant4(src[v], f);
-    if (lane == 0) scale[r] = s;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) m = absmax4(m, x[i]);
+    m = block_max(m, sh, turn);
+    float f;
+    bool bad;
+    const float s = row_quant(m, f, bad);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.codes + r * p.cols);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (tid + i * nt < n4) dst[tid + i * nt] = bad ? 0u : quant4(x[i], f);
+    if (tid == 0) p.scale[r] = s;
   }
+}
+
+// Rows that do not fit the registers (more than 16384 columns): two passes, the second from L2.
+__global__ void __launch_bounds__(1024) quant_long_rows_kernel(const QuantParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ uint32_t sh[2][32];
+  __shared__ int pref[kI8MaxGroups + 1], warp_tot[32];
+  const int n4 = p.cols / 4;
+  const RealRows rows(p, pref, warp_tot);
+  const int total = rows.total();
+  int b = 0;
+  for (int k = blockIdx.x; k < total; k += gridDim.x, b ^= 1) {
+    const long long r = rows.row(k);
+    const float4* src = reinterpret_cast<const float4*>(p.h + r * p.cols);
+    uint32_t m = 0;
+    for (int v = threadIdx.x; v < n4; v += blockDim.x) m = absmax4(m, src[v]);
+    m = block_max(m, sh, b);
+    float f;
+    bool bad;
+    const float s = row_quant(m, f, bad);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.codes + r * p.cols);
+    for (int v = threadIdx.x; v < n4; v += blockDim.x) dst[v] = bad ? 0u : quant4(src[v], f);
+    if (threadIdx.x == 0) p.scale[r] = s;
+  }
+}
+
+template <int VPT>
+cudaError_t launch_quant(const QuantParams& p, long long max_rows, cudaStream_t st) {
+  const int n4 = p.cols / 4, threads = 32 * ((n4 + 32 * VPT - 1) / (32 * VPT));
+  const int per_sm = 1024 / threads < 32 ? 1024 / threads : 32;  // (64 registers a thread)
+  const long long most = static_cast<long long>(num_sms()) * per_sm;
+  return launch_k(quant_rows_kernel<VPT>, static_cast<int>(max_rows < most ? max_rows : most), threads, 0, st, p);
 }
 
 // int8 codes as bf16 (exact), for the router's product.
@@ -237,11 +330,17 @@ cudaError_t launch_codes_to_bf16(const void* q, long long n, void* x_bf16, cudaS
 
 cudaError_t launch_quant_rows(const float* h, long long max_rows, const int32_t* offsets, const int32_t* counts, int E,
                               int cap, int cols, void* codes, float* scale, cudaStream_t st) {
-  const long long want = cdiv(max_rows, kQuantWarps);
-  const int grid = static_cast<int>(want < num_sms() * 8LL ? (want > 0 ? want : 1) : num_sms() * 8LL);
+  const QuantParams p{h, offsets, counts, E, cap, cols, static_cast<int8_t*>(codes), scale};
   trace_before(MOE_K_QUANT_H, st);
-  const cudaError_t err = launch_k(quant_rows_kernel, grid, 32 * kQuantWarps, 0, st, h, offsets, counts, E, cap, cols,
-                                   static_cast<int8_t*>(codes), scale);
+  cudaError_t err;
+  if (cols <= 512) {
+    err = launch_quant<4>(p, max_rows, st);
+  } else if (cols <= 16384) {
+    err = launch_quant<8>(p, max_rows, st);
+  } else {
+    const long long most = num_sms();
+    err = launch_k(quant_long_rows_kernel, static_cast<int>(max_rows < most ? max_rows : most), 1024, 0, st, p);
+  }
   trace_after(MOE_K_QUANT_H, st);
   return err != cudaSuccess ? err : cudaGetLastError();
 }

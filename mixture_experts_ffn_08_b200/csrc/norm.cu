@@ -64,26 +64,6 @@ MOE_DEVINL int e4m3_scale_bits(float m, float rstd_f, double rstd) {
   return e < 1 ? 1 : e;
 }
 
-// Packed fp32 pairs.
-MOE_DEVINL float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
-  return r;
-}
-MOE_DEVINL float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
-        "l"(reinterpret_cast<const unsigned long long&>(c)));
-  return r;
-}
-// max(a, |b|), NaN where either is.
-MOE_DEVINL float max_abs(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
-  return r;
-}
 MOE_DEVINL float2 unpack2(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
 // bf16(a + b) of two pairs.
 MOE_DEVINL uint32_t add_bf16x2(uint32_t a, uint32_t b) {
@@ -93,10 +73,6 @@ MOE_DEVINL uint32_t add_bf16x2(uint32_t a, uint32_t b) {
 MOE_DEVINL uint4 add8(uint4 a, uint4 b) {
   return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
 }
-MOE_DEVINL void cp_async16(void* dst_smem, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst_smem)), "l"(src) : "memory");
-}
-
 MOE_DEVINL uint32_t codes_e4m3(const float* v) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
@@ -169,9 +145,9 @@ MOE_DEVINL RowScale row_scale(double ss, uint32_t amax_bits, const NormParams& p
   return r;
 }
 
-// Stores the 8 outputs of vector v (products zw) of a row; called by whole half-warps.
+// Stores the 8 outputs of vector v (products zw) of a row, where `in`; called by whole warps.
 template <int FMT>
-MOE_DEVINL void store_vec(const float2 (&zw)[4], const RowScale& r, const NormParams& p, long long row, int v) {
+MOE_DEVINL void store_vec(const float2 (&zw)[4], const RowScale& r, const NormParams& p, long long row, int v, bool in) {
   const long long at = row * p.nvec + v;
   if constexpr (FMT == NORM_BF16) {
     const float2 f = make_float2(r.factor, r.factor);
@@ -181,13 +157,14 @@ MOE_DEVINL void store_vec(const float2 (&zw)[4], const RowScale& r, const NormPa
       const float2 y = mul2(zw[i], f);
       w[i] = pack_bf16x2(y.x, y.y);
     }
-    static_cast<uint4*>(p.out)[at] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (in) static_cast<uint4*>(p.out)[at] = make_uint4(w[0], w[1], w[2], w[3]);
   } else if constexpr (FMT == NORM_E4M3) {
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) m = max_abs(max_abs(m, zw[i].x), zw[i].y);
     // 16 lanes hold the 128 channels
-    m = __uint_as_float(__reduce_max_sync(0xffffu << (threadIdx.x & 16), __float_as_uint(m)));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(kAll, m, o));
     float2 y[4];
     float s = 1.f;
     if (r.bad || __float_as_uint(m) >= kInfBits) {
@@ -203,16 +180,18 @@ MOE_DEVINL void store_vec(const float2 (&zw)[4], const RowScale& r, const NormPa
       for (int i = 0; i < 4; ++i) y[i] = fma2(zw[i], f, mul2(zw[i], g));
     }
     const float* yv = reinterpret_cast<const float*>(y);
-    static_cast<uint2*>(p.out)[at] = make_uint2(codes_e4m3(yv), codes_e4m3(yv + 4));
-    if ((threadIdx.x & 15) == 0) p.scale[at >> 4] = s;
+    if (in) {
+      static_cast<uint2*>(p.out)[at] = make_uint2(codes_e4m3(yv), codes_e4m3(yv + 4));
+      if ((threadIdx.x & 15) == 0) p.scale[at >> 4] = s;
+    }
   } else {
     uint32_t c[8];
     if (!r.wide) {
       // (NaN and infinite products are in rows whose factor is 0 and whose codes are cleared below)
-      const float2 f = make_float2(r.factor, r.factor), magic = make_float2(12582912.f, 12582912.f);
+      const float2 f = make_float2(r.factor, r.factor);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 y = fma2(zw[i], f, magic);
+        const float2 y = fma2(zw[i], f, make_float2(kRoundMagic, kRoundMagic));
         c[2 * i] = __float_as_uint(y.x);
         c[2 * i + 1] = __float_as_uint(y.y);
       }
@@ -223,11 +202,7 @@ MOE_DEVINL void store_vec(const float2 (&zw)[4], const RowScale& r, const NormPa
         c[2 * i + 1] = static_cast<uint32_t>(__double2int_rn(static_cast<double>(zw[i].y) * r.factor_wide));
       }
     }
-    uint32_t q[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      q[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
-    static_cast<uint2*>(p.out)[at] = r.bad ? make_uint2(0u, 0u) : make_uint2(q[0], q[1]);
+    if (in) static_cast<uint2*>(p.out)[at] = r.bad ? make_uint2(0u, 0u) : make_uint2(low_bytes(c), low_bytes(c + 4));
   }
 }
 
@@ -297,6 +272,9 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(const NormParams p, con
         }
         if constexpr (HOLD_W) products<FMT>(z, w[i], zw[i], ss, amax);
         else products<FMT>(z, __ldg(p.w + v), zw[i], ss, amax);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) zw[i][j] = make_float2(0.f, 0.f);
       }
     }
     uint32_t amax_bits = __float_as_uint(amax);
@@ -305,7 +283,7 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(const NormParams p, con
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = tid + i * nt;
-      if (v < p.nvec) store_vec<FMT>(zw[i], r, p, row, v);
+      if ((v & ~31) < p.nvec) store_vec<FMT>(zw[i], r, p, row, v, v < p.nvec);
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -334,12 +312,15 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormParams p) {
   uint32_t amax_bits = __float_as_uint(amax);
   block_reduce(ss, amax_bits, sh_ss, sh_amax, 0);
   const RowScale r = row_scale<FMT>(ss, amax_bits, p, row);
-  for (int v = threadIdx.x; v < p.nvec; v += blockDim.x) {
-    uint4 z;
-    if (p.res_out != nullptr) z = p.res_out[base + v];
-    else z = p.res != nullptr ? add8(p.x[base + v], p.res[base + v]) : p.x[base + v];
-    products<FMT>(z, __ldg(p.w + v), zw, ss, amax);
-    store_vec<FMT>(zw, r, p, row, v);
+  for (int v = threadIdx.x; (v & ~31) < p.nvec; v += blockDim.x) {
+    const bool in = v < p.nvec;
+    uint4 z = make_uint4(0, 0, 0, 0);
+    if (in) {
+      if (p.res_out != nullptr) z = p.res_out[base + v];
+      else z = p.res != nullptr ? add8(p.x[base + v], p.res[base + v]) : p.x[base + v];
+    }
+    products<FMT>(z, in ? __ldg(p.w + v) : z, zw, ss, amax);
+    store_vec<FMT>(zw, r, p, row, v, in);
   }
 }
 

@@ -216,7 +216,8 @@ def skewed_ids(wl, seed, empty=0):
     (48, 384, 384, 16, 4, 0, 5), (129, 128, 640, 3, 2, 0, 0), (130, 640, 128, 4, 1, 256, 1), (40, 256, 128, 300, 8, 0, 0),
     (400, 256, 384, 3, 2, 0, 1),      # tiles of two CTAs, an odd last half
     (700, 384, 256, 4, 2, 768, 0),    # the same in the masked layout
-    (1500, 256, 256, 5, 3, 0, 2), (300, 1152, 128, 1, 1, 0, 0), (257, 128, 128, 1, 1, 0, 0)])
+    (1500, 256, 256, 5, 3, 0, 2), (300, 1152, 128, 1, 1, 0, 0), (257, 128, 128, 1, 1, 0, 0),
+    (9, 128, 16512, 2, 1, 0, 0), (70, 128, 16640, 2, 2, 128, 0), (70, 128, 4224, 4, 2, 0, 1), (70, 128, 1152, 4, 2, 128, 1)])
 def test_expert_ffn(T, H, I, E, K, cap, empty):
     wl = I8.INT8_SMALL.with_(T=T, H=H, I=I, E=E, K=K, masked_cap=cap)
     d = inputs.make_inputs(wl, seed=T, device="cuda")
