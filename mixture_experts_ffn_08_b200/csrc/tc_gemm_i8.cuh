@@ -370,30 +370,45 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA (the leader's)
-    if (leader && lane == 0) {
+    // The whole warp runs the loop and one elected lane issues: what an MMA takes stays in
+    // uniform registers.  With one lane in the loop every descriptor is moved there first, and
+    // issuing four MMAs took longer than their 512 cycles (tensor pipe 83% busy without any
+    // load or epilogue to wait for, 98% with uniform descriptors).
+    if (leader) {
       int s = 0, acc = 0;
       uint32_t ph = 0, acc_ph = 0;
       bool ok = true;
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
       for (int item = first_item; item < total && ok; item += step) {
-        if (!mbar_wait_bounded(&tempty_bar[acc], acc_ph ^ 1u, &abort_flag)) { ok = false; break; }
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tempty_bar[acc], acc_ph ^ 1u, &abort_flag));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait_bounded(&full_bar[s], ph, &abort_flag)) { ok = false; break; }
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full_bar[s], ph, &abort_flag));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + s * Cfg::STAGE_BYTES);
-          const uint32_t b0 = a0 + Cfg::A_BYTES;
+          const uint64_t da = desc0 + static_cast<uint32_t>(s * (Cfg::STAGE_BYTES >> 4));
+          const uint64_t db = da + (Cfg::A_BYTES >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < BK / 32; ++k)
-            umma_i8<CG>(d_tmem, smem_desc_sw128(a0 + k * 32), smem_desc_sw128(b0 + k * 32), IDESC, (kb | k) != 0);
-          if constexpr (PAIR) umma_commit_pair(&empty_bar[s]); else umma_commit(&empty_bar[s]);
+            for (int k = 0; k < BK / 32; ++k) umma_i8<CG>(d_tmem, da + 2 * k, db + 2 * k, IDESC, (kb | k) != 0);
+            if constexpr (PAIR) umma_commit_pair(&empty_bar[s]); else umma_commit(&empty_bar[s]);
+          }
+          __syncwarp();
           if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
-        if constexpr (PAIR) umma_commit_pair(&tfull_bar[acc]); else umma_commit(&tfull_bar[acc]);
+        if (elect_one()) {
+          if constexpr (PAIR) umma_commit_pair(&tfull_bar[acc]); else umma_commit(&tfull_bar[acc]);
+        }
+        __syncwarp();
         if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
       }
-      if constexpr (PAIR) umma_commit_pair_local(&drain_bar); else umma_commit(&drain_bar);
+      if (elect_one()) {
+        if constexpr (PAIR) umma_commit_pair_local(&drain_bar); else umma_commit(&drain_bar);
+      }
+      __syncwarp();
       volatile int* no_abort = &no_abort_sh[1];
       mbar_wait_bounded(&drain_bar, 0, no_abort);
       if (!ok || *no_abort) abort_flag = 1;
