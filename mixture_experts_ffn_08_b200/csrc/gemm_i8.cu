@@ -35,7 +35,7 @@ bool make_tmap_i8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Output [rows, cols] of 2- or 4-byte elements, row stride ld elements: boxes of 32 rows x 128
+// Output [rows, cols] of 2- or 4-byte elements, row stride ld elements: boxes of 32 rows x 64
 // bytes.  False where the rows do not start and end on 16-byte borders (the store unit clips a box
 // at such a border: it was seen to write past cols); the kernel then stores element by element.
 bool make_tmap_out(CUtensorMap* m, void* ptr, uint64_t rows, uint64_t cols, uint64_t ld, bool wide) {
@@ -46,10 +46,10 @@ bool make_tmap_out(CUtensorMap* m, void* ptr, uint64_t rows, uint64_t cols, uint
     return false;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {ld * esz};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esz), 32};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / esz), 32};
   cuuint32_t estr[2] = {1, 1};
   return fn(m, wide ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, ptr, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -66,8 +66,7 @@ cudaError_t launch_i8(const void* A, int64_t a_rows, int64_t lda, const void* b0
     return cudaErrorInvalidValue;
   CUtensorMap tout;
   const bool wide = Cfg::SWIGLU || p.out_type == MOE_OUT_FP32;
-  // (a 16-bit box is 64 columns wide, more than the narrowest tile)
-  p.tma_store = (wide || Cfg::BN >= 64) && make_tmap_out(&tout, p.out, a_rows, p.N, p.ldo, wide) ? 1 : 0;
+  p.tma_store = make_tmap_out(&tout, p.out, a_rows, p.N, p.ldo, wide) ? 1 : 0;
   if (!p.tma_store) tout = ta;  // never used then
   auto kern = tc_gemm_i8_kernel<Cfg>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);

@@ -32,7 +32,7 @@
 namespace moe {
 
 constexpr int kI8MaxGroups = 1024;
-constexpr int kI8OutBox = 32 * 128;  // bytes of an output box: 32 rows x 128 bytes
+constexpr int kI8OutBox = 32 * 64;  // bytes of an output box: 32 rows x 64 bytes
 constexpr int kI8SmallRows = 32;  // an M-tile of at most this many rows loads this many of A
 
 struct I8Params {
@@ -89,7 +89,7 @@ struct I8Cfg {
   static constexpr int B_ROWS = BN / CG;         // B rows held by each CTA
   static constexpr int B_BYTES = B_ROWS * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int OUT_BYTES = 4 * kI8OutBox;  // one box per epilogue warp
+  static constexpr int OUT_BYTES = 4 * 2 * kI8OutBox;  // two boxes per epilogue warp
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + 1024;
   static constexpr int OUT_COLS = SWIGLU ? BN / 2 : BN;
   static constexpr int TMEM_COLS = 2 * BN;       // two accumulators
@@ -154,6 +154,31 @@ MOE_DEVINL void i8_pack32(int out_type, const float (&v)[32], uint32_t (&w)[16])
   }
 }
 
+// 32 sums of a row times its scale and the columns' (cols[0..31]), plus their biases where there
+// are any: packed pairs, the columns read as vectors (the same ones in every lane).
+MOE_DEVINL void i8_scale32(const uint32_t (&r)[32], float sa, const float* cols, const float* bias, float (&v)[32]) {
+  const float2 s2 = make_float2(sa, sa);
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 c = *reinterpret_cast<const float4*>(cols + i);
+    const float2 a = mul2(make_float2(__int2float_rn(static_cast<int>(r[i])), __int2float_rn(static_cast<int>(r[i + 1]))), s2);
+    const float2 b = mul2(make_float2(__int2float_rn(static_cast<int>(r[i + 2])), __int2float_rn(static_cast<int>(r[i + 3]))), s2);
+    float2 x, y;
+    if (bias != nullptr) {
+      const float4 t = *reinterpret_cast<const float4*>(bias + i);
+      x = fma2(a, make_float2(c.x, c.y), make_float2(t.x, t.y));
+      y = fma2(b, make_float2(c.z, c.w), make_float2(t.z, t.w));
+    } else {
+      x = mul2(a, make_float2(c.x, c.y));
+      y = mul2(b, make_float2(c.z, c.w));
+    }
+    v[i] = x.x;
+    v[i + 1] = x.y;
+    v[i + 2] = y.x;
+    v[i + 3] = y.y;
+  }
+}
+
 // 32 fp32 outputs of one row, columns col .. col + 31 of which the first n are stored.
 MOE_DEVINL void i8_store32(const I8Params& p, long long row, int col, const float (&v)[32], int n) {
   const long long at = row * p.ldo + col;
@@ -210,32 +235,46 @@ MOE_DEVINL void i8_store4(const I8Params& p, long long row, int col, const float
   }
 }
 
-// ---- output boxes: 32 rows x 128 bytes, 128-byte swizzle (16-byte piece j of row r at j ^ (r & 7))
+// ---- output boxes: 32 rows x 64 bytes, 64-byte swizzle (16-byte piece j of row r at
+// j ^ (r / 2 & 3)), two per warp.
 // Direct stores of a lane's own row touch 32 lines per instruction; measured on B200 they cost
 // the 8192 x 14336 x 4096 product 16 of 345 us and the 128-expert prefill 300 of 2690 us, where
-// the TMA unit writes whole lines on its own.
-MOE_DEVINL void i8_box_put(uint8_t* box, int lane, int piece, const uint32_t* w) {
-  *reinterpret_cast<uint4*>(box + lane * 128 + ((piece ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-// The box may be written again: its last store has read it.
-MOE_DEVINL void i8_box_wait(int lane) {
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  __syncwarp();
-}
-MOE_DEVINL void i8_box_store(const CUtensorMap* m, const uint8_t* box, int lane, int col, int row) {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  __syncwarp();
-  if (lane == 0) {
+// the TMA unit writes whole segments on its own.
+struct I8Boxes {
+  uint8_t* base;
+  MOE_DEVINL void put(int i, int lane, const uint32_t* w) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4*>(base + i * kI8OutBox + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+          make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  }
+  MOE_DEVINL void send(const CUtensorMap* m, int i, int col, int row) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                      reinterpret_cast<uint64_t>(m)),
-                 "r"(col), "r"(row), "r"(smem_u32(box))
+                 "r"(col), "r"(row), "r"(smem_u32(base + i * kI8OutBox))
                  : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
-}
+  // Two boxes side by side, `width` columns each, that start at (row, col); w0, w1: 16 words of
+  // this lane's row.  The second one is left out where it starts past n_cols.
+  MOE_DEVINL void store2(const CUtensorMap* m, int lane, int row, int col, int width, int n_cols, const uint32_t* w0,
+                         const uint32_t* w1) {
+    // (this warp's earlier stores have read their boxes)
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+    put(0, lane, w0);
+    put(1, lane, w1);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      send(m, 0, col, row);
+      if (col + width < n_cols) send(m, 1, col + width, row);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  }
+};
 
 // tmA: boxes of 128 rows of A, tmA32: of 32.  tmB0 (and tmB1, the up weights of SWIGLU): boxes
-// of B_ROWS rows, or of 128 for SWIGLU.  tmOut (with p.tma_store): boxes of 32 rows x 128 bytes.
+// of B_ROWS rows, or of 128 for SWIGLU.  tmOut (with p.tma_store): boxes of 32 rows x 64 bytes.
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tc_gemm_i8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
@@ -417,7 +456,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;  // TMEM lane quadrant
     float* cols = col_sh[q];
-    uint8_t* box = smem + STAGES * Cfg::STAGE_BYTES + q * kI8OutBox;
+    I8Boxes out_boxes{smem + STAGES * Cfg::STAGE_BYTES + q * 2 * kI8OutBox};
     const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&tempty_bar[0]), 0) : 0u;
     const uint32_t tempty1 = PAIR ? mapa_shared(smem_u32(&tempty_bar[1]), 0) : 0u;
     int acc = 0;
@@ -454,50 +493,51 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           tmem_ld_32x32b_x32(tbase + 128 + c, ru);
           tmem_ld_wait(rg);
           reg_fence(ru);
+          float g[32], u[32];
+          i8_scale32(rg, sa, cols + c, nullptr, g);
+          i8_scale32(ru, sa, cols + 128 + c, nullptr, u);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float g = __int2float_rn(static_cast<int>(rg[i])) * (sa * cols[c + i]);
-            const float u = __int2float_rn(static_cast<int>(ru[i])) * (sa * cols[128 + c + i]);
-            rg[i] = __float_as_uint(silu_mul(g, u));
-          }
+          for (int i = 0; i < 32; ++i) rg[i] = __float_as_uint(silu_mul(g[i], u[i]));
           if (boxes) {
-            i8_box_wait(lane);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) i8_box_put(box, lane, j, rg + 4 * j);
-            i8_box_store(&tmOut, box, lane, col0 + c, box_row);
+            out_boxes.store2(&tmOut, lane, box_row, col0 + c, 16, p.N, rg, rg + 16);
           } else if (row_ok) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) st_global_v8(out + c + 8 * i, rg + 8 * i);
           }
         }
       } else {
+        // 64 columns at a time (32 in the narrowest tile): one wait and one fence for two boxes
+        constexpr int H = BN >= 64 ? 2 : 1;
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 32) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(tbase + c, r);
-          tmem_ld_wait(r);
+        for (int c = 0; c < BN; c += 32 * H) {
+          uint32_t r[H][32];
+#pragma unroll
+          for (int j = 0; j < H; ++j) tmem_ld_32x32b_x32(tbase + c + 32 * j, r[j]);
+          tmem_ld_wait(r[0]);
+          if constexpr (H == 2) reg_fence(r[1]);
           if (col0 + c >= p.N) continue;
-          float v[32];
+          if (boxes && p.out_type != MOE_OUT_FP32) {
+            uint32_t w[2][16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            v[i] = fmaf(__int2float_rn(static_cast<int>(r[i])), sa * cols[c + i], cols[256 + c + i]);
-          if (!boxes) {
-            if (row_ok) i8_store32(p, row, col0 + c, v, p.N - col0 - c);
-          } else if (p.out_type == MOE_OUT_FP32) {
-            i8_box_wait(lane);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) i8_box_put(box, lane, j, reinterpret_cast<const uint32_t*>(v) + 4 * j);
-            i8_box_store(&tmOut, box, lane, col0 + c, box_row);
+            for (int j = 0; j < H; ++j) {
+              float v[32];
+              i8_scale32(r[j], sa, cols + c + 32 * j, p.bias != nullptr ? cols + 256 + c + 32 * j : nullptr, v);
+              i8_pack32(p.out_type, v, w[j]);
+            }
+            out_boxes.store2(&tmOut, lane, box_row, col0 + c, 32, H == 2 ? p.N : 0, w[0], w[H - 1]);
           } else {
-            // 16-bit outputs: a box holds two steps of 32 columns
-            uint32_t w[16];
-            i8_pack32(p.out_type, v, w);
-            const int half = (c >> 5) & 1;
-            if (half == 0) i8_box_wait(lane);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) i8_box_put(box, lane, 4 * half + j, w + 4 * j);
-            if (half == 1 || col0 + c + 32 >= p.N)
-              i8_box_store(&tmOut, box, lane, col0 + c - 32 * half, box_row);
+            for (int j = 0; j < H; ++j) {
+              const int col = col0 + c + 32 * j;
+              if (col >= p.N) continue;
+              float v[32];
+              i8_scale32(r[j], sa, cols + c + 32 * j, p.bias != nullptr ? cols + 256 + c + 32 * j : nullptr, v);
+              if (boxes)
+                out_boxes.store2(&tmOut, lane, box_row, col, 16, p.N, reinterpret_cast<const uint32_t*>(v),
+                                 reinterpret_cast<const uint32_t*>(v) + 16);
+              else if (row_ok)
+                i8_store32(p, row, col, v, p.N - col);
+            }
           }
         }
       }
@@ -562,7 +602,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   constexpr uint32_t IDESC = idesc_i8_s32(128, BN);
   extern __shared__ uint8_t dsmem[];
   __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES], done_bar;
-  __shared__ float scale_sh[BN], bias_sh[BN];
+  __shared__ __align__(16) float scale_sh[BN], bias_sh[BN];
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_flag;
 
@@ -671,9 +711,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         tmem_ld_wait(r);
         if (!row_ok || col0 + c >= p.N) continue;
         float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          v[i] = fmaf(__int2float_rn(static_cast<int>(r[i])), sa * scale_sh[c + i], bias_sh[c + i]);
+        i8_scale32(r, sa, scale_sh + c, p.bias != nullptr ? bias_sh + c : nullptr, v);
         i8_store32(p, m0 + row, col0 + c, v, p.N - col0 - c);
       }
     }
