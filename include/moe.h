@@ -276,8 +276,8 @@ moe_status_t moe_shared_expert_ffn(const moe_params_t* p, const void* x, const v
 /*   NULL; out [M,N] of out_type (moe_out_type_t), rows ldo elements apart; columns past  */
 /*   N are not touched.  The sum is exact; one rounding to out_type (fp16: to infinity    */
 /*   past 65504).                                                                        */
-/* M >= 0, N >= 1 of any size; K a multiple of 16, 16..131056; lda and ldw multiples of   */
-/* 16; a and w 16-byte aligned.  No workspace.  device_status: optional device int32 that */
+/* M 0..2^30, N 1..2^30; K a multiple of 16, 16..131056; lda and ldw multiples of 16; a    */
+/* and w 16-byte aligned; out overlaps no input.  No workspace.  device_status: optional device int32 that */
 /* the caller has zeroed; MOE_DEV_TIMEOUT is OR-ed into it.                               */
 /* ---------------------------------------------------------------------------------- */
 moe_status_t moe_linear_int8(int32_t M, int32_t N, int32_t K, const void* a, int64_t lda,

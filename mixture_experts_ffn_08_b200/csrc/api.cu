@@ -844,6 +844,7 @@ moe_status_t moe_linear_int8(int32_t M, int32_t N, int32_t K, const void* a, int
   if (M < 0 || N <= 0 || K <= 0 || lda < K || ldw < K || ldo < N) return MOE_ERR_INVALID_ARG;
   if (out_type != MOE_OUT_BF16 && out_type != MOE_OUT_FP16 && out_type != MOE_OUT_FP32) return MOE_ERR_INVALID_ARG;
   if (K % 16 != 0 || K > kMaxInt8K || lda % 16 != 0 || ldw % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (M > (1 << 30) || N > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   const long long tiles = (M + 127LL) / 128 * ((N + 31LL) / 32);
   if (tiles > INT32_MAX || lda >= (1LL << 40) || ldw >= (1LL << 40)) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;

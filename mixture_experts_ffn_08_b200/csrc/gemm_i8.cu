@@ -189,7 +189,7 @@ struct RealRows {
     __syncthreads();
   }
   MOE_DEVINL int count(int g) const {
-    return p.counts != nullptr ? __ldg(p.counts + g) : __ldg(p.offsets + g + 1) - __ldg(p.offsets + g);
+    return real_rows(p.offsets, p.counts, p.cap, g);
   }
   MOE_DEVINL int total() const { return pref[p.E]; }
   // where real row i lies

@@ -145,9 +145,20 @@ MOE_DEVINL RowScale row_scale(double ss, uint32_t amax_bits, const NormParams& p
   return r;
 }
 
-// Stores the 8 outputs of vector v (products zw) of a row, where `in`; called by whole warps.
+// e4m3: the largest |z w| of the 128 channels, of which 16 lanes hold 8 each; called by whole warps.
+MOE_DEVINL float block_largest(const float2 (&zw)[4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max_abs(max_abs(m, zw[i].x), zw[i].y);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(kAll, m, o));
+  return m;
+}
+
+// Stores the 8 outputs of vector v (products zw; m: block_largest) of a row, where `in`.
 template <int FMT>
-MOE_DEVINL void store_vec(const float2 (&zw)[4], const RowScale& r, const NormParams& p, long long row, int v, bool in) {
+MOE_DEVINL void store_vec(const float2 (&zw)[4], float m, const RowScale& r, const NormParams& p, long long row, int v,
+                          bool in) {
   const long long at = row * p.nvec + v;
   if constexpr (FMT == NORM_BF16) {
     const float2 f = make_float2(r.factor, r.factor);
@@ -159,12 +170,6 @@ MOE_DEVINL void store_vec(const float2 (&zw)[4], const RowScale& r, const NormPa
     }
     if (in) static_cast<uint4*>(p.out)[at] = make_uint4(w[0], w[1], w[2], w[3]);
   } else if constexpr (FMT == NORM_E4M3) {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max_abs(max_abs(m, zw[i].x), zw[i].y);
-    // 16 lanes hold the 128 channels
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(kAll, m, o));
     float2 y[4];
     float s = 1.f;
     if (r.bad || __float_as_uint(m) >= kInfBits) {
@@ -277,13 +282,16 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(const NormParams p, con
         for (int j = 0; j < 4; ++j) zw[i][j] = make_float2(0.f, 0.f);
       }
     }
+    float m[VPT];  // (before the reduction, whose wait hides it)
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) m[i] = FMT == NORM_E4M3 ? block_largest(zw[i]) : 0.f;
     uint32_t amax_bits = __float_as_uint(amax);
     block_reduce(ss, amax_bits, sh_ss, sh_amax, b);
     const RowScale r = row_scale<FMT>(ss, amax_bits, p, row);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = tid + i * nt;
-      if ((v & ~31) < p.nvec) store_vec<FMT>(zw[i], r, p, row, v, v < p.nvec);
+      if ((v & ~31) < p.nvec) store_vec<FMT>(zw[i], m[i], r, p, row, v, v < p.nvec);
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -320,7 +328,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormParams p) {
       else z = p.res != nullptr ? add8(p.x[base + v], p.res[base + v]) : p.x[base + v];
     }
     products<FMT>(z, in ? __ldg(p.w + v) : z, zw, ss, amax);
-    store_vec<FMT>(zw, r, p, row, v, in);
+    store_vec<FMT>(zw, FMT == NORM_E4M3 ? block_largest(zw) : 0.f, r, p, row, v, in);
   }
 }
 

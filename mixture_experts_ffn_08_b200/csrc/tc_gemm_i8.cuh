@@ -109,9 +109,14 @@ struct I8Tile {
   long long row0;    // first row of the tile in A and out
 };
 
+// Real rows of group g: its count, but never more than its rows in the layout.
+MOE_DEVINL int real_rows(const int32_t* offsets, const int32_t* counts, int cap, int g) {
+  const int room = cap > 0 ? cap : __ldg(offsets + g + 1) - __ldg(offsets + g);
+  const int n = counts != nullptr ? __ldg(counts + g) : room;
+  return n < 0 ? 0 : (n < room ? n : room);
+}
 MOE_DEVINL int i8_count(const I8Params& p, int g) {
-  if (p.dense_rows > 0) return p.dense_rows;
-  return p.counts != nullptr ? __ldg(p.counts + g) : __ldg(p.offsets + g + 1) - __ldg(p.offsets + g);
+  return p.dense_rows > 0 ? p.dense_rows : real_rows(p.offsets, p.counts, p.masked_cap, g);
 }
 
 // Work item -> tile; pref[g] = NT * sum over e < g of M-tiles(e).  Inside a group the operand

@@ -264,6 +264,22 @@ def test_expert_ffn_special_rows(T):
     assert torch.isfinite(y[others]).all()
 
 
+@pytest.mark.parametrize("cap", [0, 128])
+def test_expert_ffn_counts_past_the_layout(cap):
+    """A count past its expert's rows, or a negative one, reads and writes nothing beyond them."""
+    wl = I8.INT8_SMALL.with_(T=100, E=4, K=1, masked_cap=cap)
+    d = inputs.make_inputs(wl, seed=2, device="cuda")
+    r = bucketed(wl, d, np.arange(100)[:, None] % 3)
+    y = run_ffn(wl, d, r)
+    wrong = dict(r, counts=torch.tensor([1000000, -5, int(r["counts"][2]), 999999], dtype=torch.int32, device="cuda"))
+    z = run_ffn(wl, d, wrong)
+    rows = rows_of_experts(wl, r)
+    assert torch.equal(z[rows[0]], y[rows[0]]) and torch.equal(z[rows[2]], y[rows[2]])
+    assert (z[rows[1]] == 33.0).all()
+    end = 4 * cap if cap else int(r["offs"][4])
+    assert (z[end:] == 33.0).all()
+
+
 def test_expert_ffn_same_expert_twice():
     """A token that names one expert K times fills K rows of its bucket."""
     wl = I8.INT8_SMALL.with_(T=70, E=4, K=3)

@@ -52,6 +52,7 @@ def linear(lib, M=4, N=8, K=32, a=ADDR, lda=32, sa=ADDR, w=ADDR, ldw=32, sw=ADDR
     (dict(ldw=16), INVALID), (dict(ldo=7), INVALID), (dict(kind=3), INVALID), (dict(kind=-1), INVALID),
     (dict(K=24), UNSUPPORTED), (dict(K=131072, lda=131072, ldw=131072), UNSUPPORTED), (dict(lda=40), UNSUPPORTED),
     (dict(ldw=40), UNSUPPORTED), (dict(lda=1 << 40), UNSUPPORTED), (dict(M=2**31 - 1, N=2**31 - 1, ldo=2**31), UNSUPPORTED),
+    (dict(M=2**30 + 1), UNSUPPORTED), (dict(N=2**30 + 1, ldo=2**31), UNSUPPORTED), (dict(M=2**30, N=2**30, ldo=2**30), UNSUPPORTED),
     (dict(a=None), INVALID), (dict(sa=None), INVALID), (dict(w=None), INVALID), (dict(sw=None), INVALID),
     (dict(out=None), INVALID), (dict(a=ADDR + 8), INVALID), (dict(w=ADDR + 8), INVALID), (dict(out=ADDR + 1), INVALID),
     (dict(out=ADDR + 2, kind=2), INVALID), (dict(sa=ADDR + 2), INVALID), (dict(sw=ADDR + 1), INVALID),
