@@ -3,6 +3,8 @@
 #include <cudaTypedefs.h>
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "tc_gemm_i8.cuh"
 
@@ -55,6 +57,19 @@ bool make_tmap_out(CUtensorMap* m, void* ptr, uint64_t rows, uint64_t cols, uint
 
 long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
+// Lets a kernel use `bytes` of dynamic shared memory, once per device (`done`: one bit each).
+template <class Kern>
+cudaError_t allow_smem(Kern kern, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if ((done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
+
 // A [a_rows, K] (row stride lda), B [b_rows, K] (row stride ldb; b1: SWIGLU's up weights).
 template <class Cfg>
 cudaError_t launch_i8(const void* A, int64_t a_rows, int64_t lda, const void* b0, const void* b1, int64_t b_rows,
@@ -62,14 +77,17 @@ cudaError_t launch_i8(const void* A, int64_t a_rows, int64_t lda, const void* b0
   constexpr uint32_t b_box = Cfg::SWIGLU ? 128 : Cfg::B_ROWS;
   CUtensorMap ta, ta32, tb0, tb1;
   if (!make_tmap_i8(&ta, A, a_rows, p.K, lda, 128) || !make_tmap_i8(&ta32, A, a_rows, p.K, lda, kI8SmallRows) ||
-      !make_tmap_i8(&tb0, b0, b_rows, p.K, ldb, b_box) || !make_tmap_i8(&tb1, b1, b_rows, p.K, ldb, b_box))
+      !make_tmap_i8(&tb0, b0, b_rows, p.K, ldb, b_box))
     return cudaErrorInvalidValue;
+  tb1 = tb0;  // (read by SWIGLU only)
+  if (Cfg::SWIGLU && !make_tmap_i8(&tb1, b1, b_rows, p.K, ldb, b_box)) return cudaErrorInvalidValue;
   CUtensorMap tout;
   const bool wide = Cfg::SWIGLU || p.out_type == MOE_OUT_FP32;
   p.tma_store = make_tmap_out(&tout, p.out, a_rows, p.N, p.ldo, wide) ? 1 : 0;
   if (!p.tma_store) tout = ta;  // never used then
   auto kern = tc_gemm_i8_kernel<Cfg>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+  static std::atomic<unsigned long long> smem_set{0};
+  cudaError_t err = allow_smem(kern, Cfg::SMEM_BYTES, smem_set);
   if (err != cudaSuccess) return err;
   const long long most = num_sms() / Cfg::CG;
   const long long n = max_items < most ? (max_items > 0 ? max_items : 1) : most;
@@ -109,7 +127,8 @@ cudaError_t launch_i8_split(const void* a, int64_t lda, const void* w, int64_t l
   if (!make_tmap_i8(&ta, a, M, p.K, lda, box) || !make_tmap_i8(&tb, w, p.N, p.K, ldw, Cfg::BN))
     return cudaErrorInvalidValue;
   auto kern = tc_gemm_i8_split_kernel<Cfg>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+  static std::atomic<unsigned long long> smem_set{0};
+  cudaError_t err = allow_smem(kern, Cfg::SMEM_BYTES, smem_set);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ks, static_cast<unsigned>(cdiv(p.N, Cfg::BN)), static_cast<unsigned>(cdiv(M, 128)));
@@ -183,7 +202,7 @@ struct RealRows {
     for (int w = 0; w < warp; ++w) acc += warp_tot[w];
     for (int g = g0; g < g0 + per && g < p.E; ++g) {
       pref[g] = acc;
-      acc += count(g);
+      acc += per == 1 ? run : count(g);
     }
     if (warp == warps - 1 && lane == 31) pref[p.E] = acc;
     __syncthreads();
@@ -422,10 +441,10 @@ cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, cons
   if (mt * cdiv(N, 128) > sms)
     return launch_i8<I8Cfg<1, 128, false, 6>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 128), MOE_K_LINEAR, st);
   // One round of tiles of 128 x bn over ks parts of K each: of those that fit, the one whose CTAs
-  // load the fewest operand bytes.  Exchanging the parts takes about as long as loading 300 KB does
-  // for 128 x 128 sums, and less for fewer (measured, in four parts and in one: 128 x 4096 x 1024
-  // 8.0 and 5.1 us, 128 x 4096 x 7168 13.4 and 19.9, 8 x 512 x 4096 5.4 and 11.8, 77 x 1031 x 1552
-  // 5.6 and 7.4).
+  // load the fewest operand bytes.  Exchanging the parts takes about as long as loading 140 KB does
+  // for 128 x 128 sums, and less for fewer (measured, in parts and in one: 128 x 4096 x 1024 6.7
+  // and 5.4 us, 128 x 4096 x 7168 12.1 and 17.7, 32 x 4096 x 1024 4.4 and 5.1, 8 x 512 x 4096 5.6
+  // and 11.0, 77 x 1031 x 1552 5.3 and 7.2).
   const int KB = static_cast<int>(cdiv(K, 128)), box = M <= kI8SmallRows ? kI8SmallRows : 128;
   int best_bn = 128, best_ks = 1;
   long long best = -1;
@@ -433,7 +452,7 @@ cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, cons
     for (int ks = 1; ks <= 4 && ks * 2 <= KB + 1; ks *= 2) {
       if (mt * cdiv(N, bn) * ks > sms) continue;
       const long long cost = static_cast<long long>(box + bn) * 128 * cdiv(KB, ks) +
-                             (ks > 1 ? (40 << 10) + bn * box * 16LL : 0);
+                             (ks > 1 ? (10 << 10) + bn * (box == 128 ? 1024LL : 64LL) : 0);
       if (best < 0 || cost < best) {
         best = cost;
         best_bn = bn;

@@ -19,13 +19,15 @@
 //
 // Rows: group g's real rows are the first count(g) of those that start at offsets[g] (or at
 // g * masked_cap).  The schedule comes from the counts alone: work items are (group, N-tile,
-// M-tile) with a prefix sum over the groups in shared memory, all of the same cost, and
+// M-tile) with the counts and a prefix sum over the groups in shared memory, all of the same cost, and
 // walked in steps of the grid.
 //
 // Warp roles (192 threads): warp 0 issues TMA loads into the stage ring, warp 1 allocates TMEM
 // and issues MMAs, warps 2-5 run the epilogue.  Every wait is bounded; on a timeout the CTA
 // sets MOE_DEV_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 #pragma once
+
+#include <type_traits>
 
 #include "tc_gemm_2cta.cuh"
 
@@ -98,7 +100,7 @@ struct I8Cfg {
   static_assert(BN == 32 || BN == 64 || BN == 128 || BN == 256, "two accumulators in a power of two of TMEM columns");
   static_assert(!SWIGLU || BN == 256, "a SwiGLU tile is 128 gate and 128 up rows");
   static_assert(CG == 1 || BN == 256, "pair tiles are 256 x 256");
-  static_assert(SMEM_BYTES + 4 * (kI8MaxGroups + 2) + 4 * 512 * 4 + 1024 <= 227 * 1024, "shared memory");
+  static_assert(SMEM_BYTES + 8 * (kI8MaxGroups + 1) + 4 * 512 * 4 + 512 <= 227 * 1024, "shared memory");
 };
 
 struct I8Tile {
@@ -122,7 +124,7 @@ MOE_DEVINL int i8_count(const I8Params& p, int g) {
 // Work item -> tile; pref[g] = NT * sum over e < g of M-tiles(e).  Inside a group the operand
 // with fewer rows is the one that the CTAs running side by side read again from L2.
 template <class Cfg>
-MOE_DEVINL I8Tile i8_decode(int item, int NT, const I8Params& p, const int* pref) {
+MOE_DEVINL I8Tile i8_decode(int item, int NT, const I8Params& p, const int* pref, const int* cnt) {
   int lo = 0, hi = p.G - 1;  // group with pref[g] <= item < pref[g+1]
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -130,7 +132,7 @@ MOE_DEVINL I8Tile i8_decode(int item, int NT, const I8Params& p, const int* pref
   }
   I8Tile t;
   t.group = lo;
-  t.count = i8_count(p, lo);
+  t.count = cnt[lo];
   const int tiles = (t.count + Cfg::TILE_M - 1) / Cfg::TILE_M;
   const int local = item - pref[lo];
   const bool m_outer = static_cast<long long>(tiles) * Cfg::TILE_M > static_cast<long long>(NT) * Cfg::BN;
@@ -219,27 +221,6 @@ MOE_DEVINL void i8_store1(const I8Params& p, long long row, int col, float v) {
   else static_cast<__half*>(p.out)[at] = __float2half_rn(v);
 }
 
-MOE_DEVINL void i8_store4(const I8Params& p, long long row, int col, const float (&v)[4], int n) {
-  const long long at = row * p.ldo + col;
-  if (n >= 4 && p.out_type == MOE_OUT_FP32 && (reinterpret_cast<uintptr_t>(static_cast<float*>(p.out) + at) & 15) == 0) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-  } else if (n >= 4 && p.out_type != MOE_OUT_FP32 &&
-             (reinterpret_cast<uintptr_t>(static_cast<uint16_t*>(p.out) + at) & 7) == 0) {
-    uint2 w;
-    if (p.out_type == MOE_OUT_BF16) {
-      w = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    } else {
-      const __half2 lo = __floats2half2_rn(v[0], v[1]), hi = __floats2half2_rn(v[2], v[3]);
-      w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    }
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) i8_store1(p, row, col + i, v[i]);
-  }
-}
-
 // ---- output boxes: 32 rows x 64 bytes, 64-byte swizzle (16-byte piece j of row r at
 // j ^ (r / 2 & 3)), two per warp.
 // Direct stores of a lane's own row touch 32 lines per instruction; measured on B200 they cost
@@ -292,7 +273,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   extern __shared__ uint8_t dsmem[];
   __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES];
   __shared__ uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
-  __shared__ int pref[kI8MaxGroups + 1];
+  __shared__ int pref[kI8MaxGroups + 1], cnt[kI8MaxGroups];
   __shared__ __align__(16) float col_sh[4][512];  // per epilogue warp: column scales, then biases
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_flag;
@@ -339,12 +320,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   // the counts and A come from the kernels before this one
   pdl_launch_dependents();
   pdl_wait();
+  for (int g = threadIdx.x; g < p.G; g += Cfg::THREADS) cnt[g] = i8_count(p, g);
+  __syncthreads();
   if (warp == 2) {
     // pref[] over the groups, one warp: each lane sums a contiguous run, then a scan
     const int per = (p.G + 31) / 32;
     const int g0 = lane * per;
     int run = 0;
-    for (int g = g0; g < g0 + per && g < p.G; ++g) run += NT * ((i8_count(p, g) + Cfg::TILE_M - 1) / Cfg::TILE_M);
+    for (int g = g0; g < g0 + per && g < p.G; ++g) run += NT * ((cnt[g] + Cfg::TILE_M - 1) / Cfg::TILE_M);
     int incl = run;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -354,7 +337,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     int acc = incl - run;
     for (int g = g0; g < g0 + per && g < p.G; ++g) {
       pref[g] = acc;
-      acc += NT * ((i8_count(p, g) + Cfg::TILE_M - 1) / Cfg::TILE_M);
+      acc += NT * ((cnt[g] + Cfg::TILE_M - 1) / Cfg::TILE_M);
     }
     if (lane == 31) pref[p.G] = incl;
   }
@@ -373,7 +356,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       long long issued = 0;
       bool ok = true;
       for (int item = first_item; item < total && ok; item += step) {
-        const I8Tile t = i8_decode<Cfg>(item, NT, p, pref);
+        const I8Tile t = i8_decode<Cfg>(item, NT, p, pref, cnt);
         const int a_box = i8_box_rows(t.count - t.m0 - 128 * static_cast<int>(rank));
         uint32_t tx = static_cast<uint32_t>(a_box) * BK + Cfg::B_BYTES;
         if (PAIR) tx += static_cast<uint32_t>(i8_box_rows(t.count - t.m0 - 128)) * BK + Cfg::B_BYTES;  // (the leader's)
@@ -467,7 +450,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     int acc = 0;
     uint32_t acc_ph = 0;
     for (int item = first_item; item < total; item += step) {
-      const I8Tile t = i8_decode<Cfg>(item, NT, p, pref);
+      const I8Tile t = i8_decode<Cfg>(item, NT, p, pref, cnt);
       const int col0 = t.n_tile * Cfg::OUT_COLS;
       const long long wrow = static_cast<long long>(t.group) * p.N + col0;
       const int in_tile = 128 * static_cast<int>(rank) + q * 32 + lane;
@@ -584,18 +567,73 @@ struct I8SplitCfg {
   static constexpr int BK = 128;
   static constexpr int A_BYTES = 128 * BK;
   static constexpr int STAGE_BYTES = A_BYTES + BN * BK;
-  // received parts: [part][column group of 4][row] int4, 512 contiguous bytes per warp and access
+  // received parts: [part][column group of 4][row ^ (group & 7)] int4: a warp's push (a lane per
+  // row) is 512 contiguous bytes, and lanes that read along a row meet no bank twice
   static constexpr int PART_BYTES = 128 * BN * 4;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + PART_BYTES + 1024;
   static constexpr int TMEM_COLS = BN;
   static constexpr int THREADS = 192;
-  static_assert(SMEM_BYTES + 2 * BN * 4 + 1024 <= 227 * 1024, "shared memory");
+  static_assert(SMEM_BYTES + 2 * BN * 4 + 2048 <= 227 * 1024, "shared memory");
 };
 
 MOE_DEVINL void st_cluster_v4(uint32_t addr, const uint32_t* v) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3])
                : "memory");
+}
+
+// Adds the KS parts of this CTA's 4 * groups columns from `col` on and stores them, `rows` rows from
+// m0 on.  128 threads, lanes along a row: thread t keeps column group t % groups and takes every
+// (128 / groups)th row.  KS and the output type are fixed at compile time: a CTA has one such warp
+// per scheduler, so the stage takes as long as its instructions (with them in registers, and four
+// rows at a time, 1 us instead of 3).
+template <int KS, int TYPE>
+MOE_DEVINL void i8_finish_parts(const I8Params& p, const uint8_t* parts, int t, int log_groups, int m0, int rows, int col,
+                                const float* scale, const float* bias, const float* row_scale) {
+  using Word = typename std::conditional<TYPE == MOE_OUT_FP32, float4, uint2>::type;
+  constexpr int ESZ = TYPE == MOE_OUT_FP32 ? 4 : 2;
+  const int groups = 1 << log_groups, g = t & (groups - 1);
+  col += 4 * g;
+  if (col >= p.N) return;
+  const float4 sw = *reinterpret_cast<const float4*>(scale + 4 * g);
+  const float4 sb = *reinterpret_cast<const float4*>(bias + 4 * g);
+  uint8_t* out = static_cast<uint8_t*>(p.out) + (m0 * p.ldo + col) * ESZ;
+  const int64_t pitch = p.ldo * ESZ;
+  const bool vec = p.N - col >= 4 && ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(pitch)) & (sizeof(Word) - 1)) == 0;
+  const uint8_t* at = parts + g * 2048;
+  const int part_bytes = groups * 2048, swz = g & 7;
+#pragma unroll 4
+  for (int r = t >> log_groups; r < rows; r += 128 >> log_groups) {
+    int4 a[KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) a[k] = *reinterpret_cast<const int4*>(at + k * part_bytes + ((r ^ swz) << 4));
+#pragma unroll
+    for (int k = 1; k < KS; ++k) {
+      a[0].x += a[k].x; a[0].y += a[k].y; a[0].z += a[k].z; a[0].w += a[k].w;
+    }
+    const float2 s2 = make_float2(row_scale[r], row_scale[r]);
+    const float2 lo = fma2(mul2(make_float2(__int2float_rn(a[0].x), __int2float_rn(a[0].y)), s2), make_float2(sw.x, sw.y),
+                           make_float2(sb.x, sb.y));
+    const float2 hi = fma2(mul2(make_float2(__int2float_rn(a[0].z), __int2float_rn(a[0].w)), s2), make_float2(sw.z, sw.w),
+                           make_float2(sb.z, sb.w));
+    if (vec) {
+      Word w;
+      if constexpr (TYPE == MOE_OUT_FP32) {
+        w = make_float4(lo.x, lo.y, hi.x, hi.y);
+      } else if constexpr (TYPE == MOE_OUT_BF16) {
+        w = make_uint2(pack_bf16x2(lo.x, lo.y), pack_bf16x2(hi.x, hi.y));
+      } else {
+        const __half2 l = __floats2half2_rn(lo.x, lo.y), h = __floats2half2_rn(hi.x, hi.y);
+        w = make_uint2(*reinterpret_cast<const uint32_t*>(&l), *reinterpret_cast<const uint32_t*>(&h));
+      }
+      *reinterpret_cast<Word*>(out + r * pitch) = w;
+    } else {
+      const float v[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < p.N - col) i8_store1(p, m0 + r, col + i, v[i]);
+    }
+  }
 }
 
 // Grid: (KS, N-tiles, M-tiles), clusters of KS.
@@ -607,7 +645,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   constexpr uint32_t IDESC = idesc_i8_s32(128, BN);
   extern __shared__ uint8_t dsmem[];
   __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES], done_bar;
-  __shared__ __align__(16) float scale_sh[BN], bias_sh[BN];
+  __shared__ __align__(16) float scale_sh[BN], bias_sh[BN], row_sh[128];
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_flag;
 
@@ -670,25 +708,28 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       if (no_abort) abort_flag = 1;
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(&full_bar[s], ph, &abort_flag)) break;
-        tc_fence_after();
-        const uint32_t a0 = smem_u32(smem + s * Cfg::STAGE_BYTES);
-        const uint32_t b0 = a0 + Cfg::A_BYTES;
+    // (the whole warp in the loop, one lane issues: see tc_gemm_i8_kernel)
+    int s = 0;
+    uint32_t ph = 0;
+    const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full_bar[s], ph, &abort_flag))) break;
+      tc_fence_after();
+      const uint64_t da = desc0 + static_cast<uint32_t>(s * (Cfg::STAGE_BYTES >> 4));
+      const uint64_t db = da + (Cfg::A_BYTES >> 4);
+      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < BK / 32; ++k)
-          umma_i8<1>(tmem_base, smem_desc_sw128(a0 + k * 32), smem_desc_sw128(b0 + k * 32), IDESC, kb != kb0 || k != 0);
+        for (int k = 0; k < BK / 32; ++k) umma_i8<1>(tmem_base, da + 2 * k, db + 2 * k, IDESC, kb != kb0 || k != 0);
         umma_commit(&empty_bar[s]);
-        if (++s == STAGES) { s = 0; ph ^= 1u; }
       }
-      umma_commit(&done_bar);
-      volatile int no_abort = 0;
-      mbar_wait_bounded(&done_bar, 0, &no_abort);
-      if (no_abort) abort_flag = 1;
+      __syncwarp();
+      if (++s == STAGES) { s = 0; ph ^= 1u; }
     }
+    if (elect_one()) umma_commit(&done_bar);
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait_bounded(&done_bar, 0, &no_abort);
+    if (no_abort) abort_flag = 1;
   }
   if (warp >= 2) {
     for (int c = threadIdx.x - 64; c < BN; c += 128) {
@@ -696,6 +737,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       scale_sh[c] = in ? __ldg(p.w_scale + col0 + c) : 0.f;
       bias_sh[c] = in && p.bias != nullptr ? __ldg(p.bias + col0 + c) : 0.f;
     }
+    const int r = threadIdx.x - 64;
+    row_sh[r] = m0 + r < p.dense_rows ? __ldg(p.a_scale + m0 + r) : 0.f;
   }
   // the products and the copies are done, or were given up
   __syncwarp();
@@ -705,61 +748,60 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   const int q = warp & 3;
   const int row = q * 32 + lane;
   const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-  if (ks == 1) {
-    const bool row_ok = m0 + row < p.dense_rows;
+  // groups of four columns that a CTA finishes: BN / ks columns, 8 at least
+  const int log_groups = 29 - __clz(BN / ks), groups = 1 << log_groups;
+  if (ks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // a lone CTA stores its rows straight from TMEM where they are whole 32-byte sectors (128 x 7168 x
+  // 4096 12.0 us against 13.1 by way of shared memory; with unaligned rows 200 x 3000 x 2000 12.9
+  // against 9.2)
+  const int esz = p.out_type == MOE_OUT_FP32 ? 4 : 2;
+  const bool direct = ks == 1 && ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.ldo * esz)) & 31) == 0;
+  if (direct) {
     if (warp >= 2 && m0 + q * 32 < p.dense_rows) {
-      const float sa = row_ok ? __ldg(p.a_scale + m0 + row) : 0.f;
+      const float sa = row_sh[row];
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(tbase + c, r);
         tmem_ld_wait(r);
-        if (!row_ok || col0 + c >= p.N) continue;
+        if (m0 + row >= p.dense_rows || col0 + c >= p.N) continue;
         float v[32];
         i8_scale32(r, sa, scale_sh + c, p.bias != nullptr ? bias_sh + c : nullptr, v);
         i8_store32(p, m0 + row, col0 + c, v, p.N - col0 - c);
       }
     }
-  } else {
-    const int log_cols = 31 - __clz(BN / ks), cols = 1 << log_cols;  // columns that a CTA finishes, 8 at least
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (warp >= 2 && m0 + q * 32 < p.dense_rows) {
-      const uint32_t mine = smem_u32(parts) + part * (cols * 512) + row * 16;
+  } else if (warp >= 2 && m0 + q * 32 < p.dense_rows) {
+    const uint32_t mine = smem_u32(parts) + part * groups * 2048;
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tbase + c, r);
-        tmem_ld_wait(r);
+    for (int c = 0; c < BN; c += 32) {
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(tbase + c, r);
+      tmem_ld_wait(r);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const int owner = (c + i) >> log_cols;
-          st_cluster_v4(mapa_shared(mine + (((c + i) & (cols - 1)) >> 2) * 2048, owner), r + i);
-        }
+      for (int i = 0; i < 32; i += 4) {
+        const int g = ((c + i) >> 2) & (groups - 1);
+        const uint32_t to = mine + g * 2048 + ((row ^ (g & 7)) << 4);
+        st_cluster_v4(ks > 1 ? mapa_shared(to, (c + i) >> (log_groups + 2)) : to, r + i);
       }
     }
-    __syncwarp();
-    cluster_sync();
-    if (warp >= 2) {
-      // a thread per row, or four warps that share 32 rows' column groups
-      const bool narrow = a_box == kI8SmallRows;
-      const int r0 = narrow ? lane : row, step = narrow ? 4 : 1;
-      if (m0 + r0 < p.dense_rows) {
-        const float sa = __ldg(p.a_scale + m0 + r0);
-        for (int g = narrow ? q : 0; g < cols / 4; g += step) {
-          const int c = part * cols + 4 * g;
-          if (col0 + c >= p.N) break;
-          int t[4] = {0, 0, 0, 0};
-          for (int k = 0; k < ks; ++k) {
-            const int4 v = *reinterpret_cast<const int4*>(parts + k * (cols * 512) + g * 2048 + r0 * 16);
-            t[0] += v.x; t[1] += v.y; t[2] += v.z; t[3] += v.w;
-          }
-          float v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = fmaf(__int2float_rn(t[i]), sa * scale_sh[c + i], bias_sh[c + i]);
-          i8_store4(p, m0 + r0, col0 + c, v, p.N - col0 - c);
-        }
-      }
-    }
+  }
+  __syncwarp();
+  if (ks > 1) cluster_sync(); else __syncthreads();
+  if (warp >= 2 && !direct) {
+    const int t = threadIdx.x - 64, first = part * 4 * groups;
+    const int rows = p.dense_rows - m0 < 128 ? p.dense_rows - m0 : 128;
+    auto finish = [&](auto ks_c) {
+      constexpr int KS = decltype(ks_c)::value;
+      if (p.out_type == MOE_OUT_BF16)
+        i8_finish_parts<KS, MOE_OUT_BF16>(p, parts, t, log_groups, m0, rows, col0 + first, scale_sh + first, bias_sh + first, row_sh);
+      else if (p.out_type == MOE_OUT_FP16)
+        i8_finish_parts<KS, MOE_OUT_FP16>(p, parts, t, log_groups, m0, rows, col0 + first, scale_sh + first, bias_sh + first, row_sh);
+      else
+        i8_finish_parts<KS, MOE_OUT_FP32>(p, parts, t, log_groups, m0, rows, col0 + first, scale_sh + first, bias_sh + first, row_sh);
+    };
+    if (ks == 1) finish(std::integral_constant<int, 1>());
+    else if (ks == 2) finish(std::integral_constant<int, 2>());
+    else finish(std::integral_constant<int, 4>());
   }
   __syncthreads();
   if (abort_flag && threadIdx.x == 0) set_status(p.status, MOE_DEV_TIMEOUT);
