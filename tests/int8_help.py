@@ -43,7 +43,8 @@ def ffn_rows(x, wg, wu, wd):
     1.16 |g| units in the last place) and division (2): below 2e-5 for |g| <= 40, where every
     test stays, and the row's scale with it.  So a code may be the neighbouring one only where
     h / s lies within 2 DELTA of itself from a border, and then y moves by one step times that
-    column of W_down.  Beside that there are the scale's own DELTA and the rounding to bf16.
+    column of W_down.  Beside that there are the scale's own DELTA and the rounding to bf16, half a
+    step of what the kernel computed, |y| and what codes moved it by.
     The last term is the reference's own: the kernel's sum over q is an exact integer and may be
     exactly 0, where the I products q s w added in fp64 leave up to I 2^-53 of their sizes' sum."""
     delta = 2e-5
@@ -56,7 +57,8 @@ def ffn_rows(x, wg, wu, wd):
     q = np.round(v) * s
     y = q @ wd.T
     own = (np.abs(q) @ np.abs(wd).T) * (q.shape[1] + 4) * 2.0 ** -53
-    return y, np.abs(y) * (2.0 ** -8 + 2 * delta) + s * (near @ np.abs(wd).T) + own + 1e-37
+    moved = s * (near @ np.abs(wd).T)
+    return y, np.abs(y) * (2.0 ** -8 + 2 * delta) + moved * (1 + 2.0 ** -8) + own + 1e-37
 
 
 def check_ffn(y, rows_of, x, weights, what=""):

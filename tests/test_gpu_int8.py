@@ -56,7 +56,7 @@ def test_linear_sizes(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(1100, 4200, 272), (2048, 2560, 1024), (2500, 2049, 144), (513, 9500, 80), (5000, 300, 64),
-                                   (257, 2600, 4096), (20000, 40, 16)])
+                                   (257, 2600, 4096), (20000, 40, 16), (100, 20000, 64), (16, 40000, 128)])
 @pytest.mark.parametrize("dtype", list(KIND))
 def test_linear_large(M, N, K, dtype):
     args, ref, tol = linear_case(M, N, K, dtype, pad=(32, 0, 3 if dtype == torch.bfloat16 else 8), seed=M)
@@ -214,8 +214,10 @@ def skewed_ids(wl, seed, empty=0):
 @pytest.mark.parametrize("T,H,I,E,K,cap,empty", [
     (1, 128, 128, 1, 1, 0, 0), (1, 256, 128, 8, 2, 0, 0), (1, 256, 256, 8, 2, 128, 0), (33, 256, 128, 8, 2, 128, 3),
     (48, 384, 384, 16, 4, 0, 5), (129, 128, 640, 3, 2, 0, 0), (130, 640, 128, 4, 1, 256, 1), (40, 256, 128, 300, 8, 0, 0),
-    (400, 256, 384, 3, 2, 0, 1),      # tiles of two CTAs, an odd last half
+    (400, 256, 384, 3, 2, 0, 1),      # several M-tiles, an odd last one
     (700, 384, 256, 4, 2, 768, 0),    # the same in the masked layout
+    (2000, 2560, 1280, 5, 2, 0, 1),   # enough tiles for pairs of CTAs in both products
+    (2000, 2560, 1280, 5, 2, 2048, 0),
     (1500, 256, 256, 5, 3, 0, 2), (300, 1152, 128, 1, 1, 0, 0), (257, 128, 128, 1, 1, 0, 0),
     (9, 128, 16512, 2, 1, 0, 0), (70, 128, 16640, 2, 2, 128, 0), (70, 128, 4224, 4, 2, 0, 1), (70, 128, 1152, 4, 2, 128, 1)])
 def test_expert_ffn(T, H, I, E, K, cap, empty):
