@@ -52,6 +52,7 @@ struct I8Params {
   void* out;               // SWIGLU: fp32 [rows, ldo]; else out_type
   int out_type;            // moe_out_type_t
   int tma_store;           // the output's tensor map is usable (16-byte aligned rows)
+  int prefetch;            // few rows: all blocks are resident at once
   int64_t ldo;
   int32_t* status;
 };
@@ -833,10 +834,18 @@ template <int M, int R>
 __global__ void __launch_bounds__(256) i8_gemv_kernel(const int8_t* __restrict__ a, int64_t lda,
                                                       const int8_t* __restrict__ w, int64_t ldw, const I8Params p) {
   pdl_launch_dependents();
-  pdl_wait();
   constexpr int UNROLL = M == 1 ? 16 : 4;
   const int lane = lane_id();
   const int n0 = (blockIdx.x * 8 + warp_id()) * R;
+  // The first 4 KB of the warp's weights on their way into L2 while the kernel before this one still
+  // runs, where all blocks are resident at once.  A prefetch is not a read: whatever that kernel
+  // writes there is what is loaded below.
+  if (p.prefetch) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (n0 + r < p.N && 128 * lane < p.K) asm volatile("prefetch.global.L2 [%0];" ::"l"(w + (n0 + r) * ldw + 128 * lane));
+  }
+  pdl_wait();
   if (n0 >= p.N) return;  // warp-uniform
   const int nvec = p.K / 16;
   int acc[R][M];

@@ -448,6 +448,29 @@ def test_norm_layer_is_the_norm_and_the_layer(dtype, T):
     assert len(seen) == B.moe_layer_launch_count(p) + 1 and seen[0] == B.K_NORM
 
 
+@pytest.mark.parametrize("dtype", [W.DTYPE_FP8, W.DTYPE_INT8])
+def test_norm_layer_keeps_a_bad_token_to_itself(dtype):
+    """One token with a NaN: the other tokens' outputs are the ones without it, bit for bit."""
+    wl = W.Workload("norm_layer", T=90, H=256, I=128, E=4, K=2, dtype=dtype)
+    d = inputs.make_inputs(wl, seed=9, device="cuda")
+    g = I8.gen(9)
+    x = torch.randn((wl.T, wl.H), generator=g, device="cuda").bfloat16()
+    w = torch.ones(wl.H, device="cuda").bfloat16()
+    p = B.params(wl)
+    ws = torch.empty(B.moe_workspace_size_norm(p), dtype=torch.uint8, device="cuda")
+    outs = []
+    for bad in (False, True):
+        if bad:
+            x[17, 3] = float("nan")
+        B.check(B.moe_clear_device_status(ws))
+        out = torch.zeros_like(x)
+        B.check(B.moe_norm_layer_forward(p, x, None, w, 1e-6, None, *I8.layer_args(d)[2:], out, None, None, None, ws, ws.numel()))
+        torch.cuda.synchronize()
+        outs.append(out)
+    rest = torch.arange(wl.T, device="cuda") != 17
+    assert torch.equal(outs[0][rest], outs[1][rest])
+
+
 def test_two_layers_in_a_row():
     """Two int8 layers as a decoder runs them: the residual stream and the norms between, against
     the chain in 64 bits on the kernels' own routing.  The bound is the layers' own, twice."""
