@@ -464,9 +464,14 @@ cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, cons
         best_ks = ks;
       }
     }
-  if (best_bn == 32) return launch_i8_split<I8SplitCfg<32, 9>>(a, lda, w, ldw, p, best_ks, st);
-  if (best_bn == 64) return launch_i8_split<I8SplitCfg<64, 7>>(a, lda, w, ldw, p, best_ks, st);
-  return launch_i8_split<I8SplitCfg<128, 4>>(a, lda, w, ldw, p, best_ks, st);
+  if (best_ks == 1) {
+    if (best_bn == 32) return launch_i8_split<I8SplitCfg<32, 10, true>>(a, lda, w, ldw, p, 1, st);
+    if (best_bn == 64) return launch_i8_split<I8SplitCfg<64, 8, true>>(a, lda, w, ldw, p, 1, st);
+    return launch_i8_split<I8SplitCfg<128, 6, true>>(a, lda, w, ldw, p, 1, st);
+  }
+  if (best_bn == 32) return launch_i8_split<I8SplitCfg<32, 9, false>>(a, lda, w, ldw, p, best_ks, st);
+  if (best_bn == 64) return launch_i8_split<I8SplitCfg<64, 7, false>>(a, lda, w, ldw, p, best_ks, st);
+  return launch_i8_split<I8SplitCfg<128, 4, false>>(a, lda, w, ldw, p, best_ks, st);
 }
 
 }  // namespace moe

@@ -561,7 +561,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 // integer), scales and stores them.  No workspace, no atomics, one launch.
 // Measured on B200, 128 x 7168 x 4096: reading the parts from the peers instead of having them
 // pushed cost 5 us more.
-template <int BN_, int STAGES_>
+// LONE: one part, whose sums may go into the stage ring (others' could arrive while it is in use).
+template <int BN_, int STAGES_, bool LONE_>
 struct I8SplitCfg {
   static constexpr int BN = BN_;
   static constexpr int STAGES = STAGES_;
@@ -571,7 +572,9 @@ struct I8SplitCfg {
   // received parts: [part][column group of 4][row ^ (group & 7)] int4: a warp's push (a lane per
   // row) is 512 contiguous bytes, and lanes that read along a row meet no bank twice
   static constexpr int PART_BYTES = 128 * BN * 4;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + PART_BYTES + 1024;
+  static constexpr bool LONE = LONE_;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + (LONE ? 0 : PART_BYTES) + 1024;
+  static_assert(PART_BYTES <= STAGES * STAGE_BYTES, "the sums fit the ring");
   static constexpr int TMEM_COLS = BN;
   static constexpr int THREADS = 192;
   static_assert(SMEM_BYTES + 2 * BN * 4 + 2048 <= 227 * 1024, "shared memory");
@@ -653,8 +656,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   const int warp = warp_id(), lane = lane_id();
   const uint32_t pad = (1024u - (smem_u32(dsmem) & 1023u)) & 1023u;
   uint8_t* smem = dsmem + pad;
-  uint8_t* parts = smem + STAGES * Cfg::STAGE_BYTES;
-  const int ks = gridDim.x, part = blockIdx.x;  // the cluster spans the grid's x
+  uint8_t* parts = smem + (Cfg::LONE ? 0 : STAGES * Cfg::STAGE_BYTES);
+  const int ks = Cfg::LONE ? 1 : gridDim.x, part = blockIdx.x;  // the cluster spans the grid's x
   const int KB = (p.K + BK - 1) / BK;
   int kb0, kb1;
   k_slice(part, ks, KB, kb0, kb1);
@@ -800,7 +803,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       else
         i8_finish_parts<KS, MOE_OUT_FP32>(p, parts, t, log_groups, m0, rows, col0 + first, scale_sh + first, bias_sh + first, row_sh);
     };
-    if (ks == 1) finish(std::integral_constant<int, 1>());
+    if constexpr (Cfg::LONE) finish(std::integral_constant<int, 1>());
     else if (ks == 2) finish(std::integral_constant<int, 2>());
     else finish(std::integral_constant<int, 4>());
   }
