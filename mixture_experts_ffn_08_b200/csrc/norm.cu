@@ -338,7 +338,9 @@ cudaError_t launch_rows(const NormParams& p, int T, cudaStream_t st) {
   const int smem = 2 * (p.res != nullptr ? 2 : 1) * VPT * threads * 16;
   auto kern = norm_rows_kernel<FMT, VPT>;
   if (smem > 40 * 1024) {
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (always the most that any row takes: a smaller one could come between another thread's two calls)
+    constexpr int most_smem = 2 * 2 * VPT * (VPT == 4 ? 832 : 1024) * 16;
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
     if (err != cudaSuccess) return err;
   }
   // blocks per SM: by shared memory, by threads (1536 leave 42 registers each), 16 at most

@@ -71,9 +71,9 @@ def check(fmt, x, r, w, out, scale, eps=EPS):
 
 @pytest.mark.parametrize("fmt", list(FORMATS))
 @pytest.mark.parametrize("T,H", [(1, 128), (1, 7168), (3, 384), (5, 8192), (2, 8320), (700, 1152), (1500, 4224),
-                                 (2, 32768), (2, 32896)])
+                                 (2, 16384), (2, 16512), (300, 20608), (3, 26624), (2, 26752), (2, 32896)])
 def test_formula(fmt, T, H):
-    """Sizes of every variant: one vector per thread, four, and rows past the registers."""
+    """Sizes of every variant: one vector per thread, two, four, and rows past the registers."""
     for residual in (True, False):
         x, r, w = inputs(T, H, seed=T + H, residual=residual)
         out, scale = outputs(T, H, fmt)
@@ -85,7 +85,7 @@ def test_formula(fmt, T, H):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
-@pytest.mark.parametrize("T,H", [(4, 1024), (600, 1024), (3, 33024)])
+@pytest.mark.parametrize("T,H", [(4, 1024), (600, 1024), (200, 16640), (3, 33024)])
 def test_in_place_and_without_the_sum(fmt, T, H):
     x, r, w = inputs(T, H, seed=3)
     p = params(T, H, fmt)
@@ -190,6 +190,36 @@ def test_streams_and_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(scale, want_s)
+
+
+def test_two_threads():
+    """Rows of different lengths from two threads at once, each on its own stream."""
+    import threading
+    failed = []
+
+    def run(H):
+        x, r, w = inputs(200, H, seed=H)
+        p = params(200, H, "int8")
+        want, want_s = outputs(200, H, "int8")
+        B.check(B.moe_add_rms_norm(p, x, r, w, EPS, None, want, want_s))
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        out, scale = outputs(200, H, "int8")
+        torch.cuda.synchronize()
+        try:
+            for _ in range(300):
+                B.check(B.moe_add_rms_norm(p, x, r, w, EPS, None, out, scale, s))
+            s.synchronize()
+            assert torch.equal(out, want) and torch.equal(scale, want_s)
+        except Exception as e:  # (a thread's exception is otherwise lost)
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(H,)) for H in (8192, 16384)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
 
 
 def test_feeds_the_e4m3_layer():
