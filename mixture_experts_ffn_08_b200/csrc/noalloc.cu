@@ -52,6 +52,7 @@ moe_status_t scratch_for_current_device(int32_t** out) {
   return MOE_OK;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
@@ -69,7 +70,8 @@ extern "C" moe_status_t moe_permute_noalloc(const moe_params_t* p, const int32_t
   if ((!empty && (!topk_ids || !x || !row_of_pair)) || !counts || !offsets_padded || !pair_of_row || !x_perm)
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(x_perm)) return MOE_ERR_INVALID_ARG;
-  if (x_scales_per_row(*p) > 0 && ((!empty && !x_scale) || !x_perm_scale)) return MOE_ERR_INVALID_ARG;
+  if (x_scales_per_row(*p) > 0 && ((!empty && !x_scale) || !x_perm_scale || !aligned4(x_scale) || !aligned4(x_perm_scale)))
+    return MOE_ERR_INVALID_ARG;
   const long long pairs = static_cast<long long>(p->T) * p->K;
   const long long chunks = (pairs + kPermChunk - 1) / kPermChunk;
   if ((chunks > 0 ? chunks : 1) * p->E > kNoAllocScratchInts) return MOE_ERR_UNSUPPORTED;

@@ -332,7 +332,7 @@ def test_expert_ffn_streams_and_graphs():
 
 # -------------------------------------------------------------------------------------- layer
 LAYERS = [dict(), dict(T=1), dict(T=5, E=300, K=8, n_group=4, topk_group=2, group_topn=2, score_fn=W.SCORE_SIGMOID, has_bias=True),
-          dict(T=300, E=4, masked_cap=384), dict(T=700, E=4, H=512, I=384), dict(T=40, skewed=True, E=16)]
+          dict(T=300, E=4, masked_cap=384), dict(T=700, E=4, H=512, I=384), dict(T=1100, E=4), dict(T=40, skewed=True, E=16)]
 
 
 @pytest.mark.parametrize("change", LAYERS, ids=str)
@@ -354,6 +354,16 @@ def test_layer(change):
     out = torch.empty_like(r["out"])
     B.check(B.moe_combine(B.params(wl), y, b["rop"], r["w"], None, out))
     assert torch.equal(out, r["out"]) and torch.equal(b["counts"], r["counts"])
+
+
+def test_layer_masked_overflow():
+    """An expert with more pairs than its rows keeps the first ones; the others add nothing."""
+    wl = I8.INT8_SMALL.with_(T=300, E=1, K=1, masked_cap=128)
+    d = inputs.make_inputs(wl, seed=6, device="cuda")
+    r = I8.run_layer(wl, d)
+    assert B.moe_get_device_status(r["ws"]) == B.MOE_DEV_CAPACITY and r["counts"].tolist() == [128]
+    full = I8.run_layer(wl.with_(masked_cap=0), d)
+    assert torch.equal(r["out"][:128], full["out"][:128]) and (r["out"][128:] == 0).all()
 
 
 def test_layer_from_host_memory():
