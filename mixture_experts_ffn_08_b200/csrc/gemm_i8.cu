@@ -118,13 +118,13 @@ cudaError_t launch_i8(const void* A, int64_t a_rows, int64_t lda, const void* b0
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-// One tile per cluster of ks CTAs; A's boxes hold 32 rows where M is at most that.
+// One tile per cluster of ks CTAs.
 template <class Cfg>
 cudaError_t launch_i8_split(const void* a, int64_t lda, const void* w, int64_t ldw, const I8Params& p, int ks,
                             cudaStream_t st) {
-  const int M = p.dense_rows, box = M <= kI8SmallRows ? kI8SmallRows : 128;
+  const int M = p.dense_rows;
   CUtensorMap ta, tb;
-  if (!make_tmap_i8(&ta, a, M, p.K, lda, box) || !make_tmap_i8(&tb, w, p.N, p.K, ldw, Cfg::BN))
+  if (!make_tmap_i8(&ta, a, M, p.K, lda, Cfg::ROWS) || !make_tmap_i8(&tb, w, p.N, p.K, ldw, Cfg::BN))
     return cudaErrorInvalidValue;
   auto kern = tc_gemm_i8_split_kernel<Cfg>;
   static std::atomic<unsigned long long> smem_set{0};
@@ -145,9 +145,33 @@ cudaError_t launch_i8_split(const void* a, int64_t lda, const void* w, int64_t l
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   trace_before(MOE_K_LINEAR, st);
-  err = cudaLaunchKernelEx(&cfg, kern, ta, tb, box, p);
+  err = cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
   trace_after(MOE_K_LINEAR, st);
   return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+// As many stages as shared memory holds, of two K-blocks each but for the largest.
+template <int BN, int ROWS, bool LONE>
+constexpr int split_sub() { return BN == 128 && ROWS == 128 ? 1 : 2; }
+template <int BN, int ROWS, bool LONE>
+constexpr int split_stages() {
+  constexpr int n = (224 * 1024 - 2 * BN * 4 - 3072 - (LONE ? 0 : ROWS * BN * 4)) / (split_sub<BN, ROWS, LONE>() * (ROWS + BN) * 128);
+  return n < 12 ? n : 12;
+}
+template <int BN, int ROWS, bool LONE>
+using SplitCfg = I8SplitCfg<BN, ROWS, split_sub<BN, ROWS, LONE>(), split_stages<BN, ROWS, LONE>(), LONE>;
+
+template <int ROWS>
+cudaError_t launch_i8_split_rows(const void* a, int64_t lda, const void* w, int64_t ldw, const I8Params& p, int bn, int ks,
+                                 cudaStream_t st) {
+  if (ks == 1) {
+    if (bn == 32) return launch_i8_split<SplitCfg<32, ROWS, true>>(a, lda, w, ldw, p, 1, st);
+    if (bn == 64) return launch_i8_split<SplitCfg<64, ROWS, true>>(a, lda, w, ldw, p, 1, st);
+    return launch_i8_split<SplitCfg<128, ROWS, true>>(a, lda, w, ldw, p, 1, st);
+  }
+  if (bn == 32) return launch_i8_split<SplitCfg<32, ROWS, false>>(a, lda, w, ldw, p, ks, st);
+  if (bn == 64) return launch_i8_split<SplitCfg<64, ROWS, false>>(a, lda, w, ldw, p, ks, st);
+  return launch_i8_split<SplitCfg<128, ROWS, false>>(a, lda, w, ldw, p, ks, st);
 }
 
 template <int M, int R>
@@ -428,50 +452,51 @@ cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, cons
   p.ldo = ldo;
   p.status = status;
   const long long sms = num_sms();
-  // One row, or two, or three and four of few channels (those read each row of A once per
-  // channel): dot products.  Measured: 2 x 4096 x 7168 8.0 us against 10.0 with the tensor cores,
-  // 4 x 512 x 4096 3.3 against 5.4, but 4 x 4096 x 7168 10.8 against 10.0.  Two channels per warp
-  // where that still leaves every SM eight warps of four: 2 x 14336 x 4096 13.6 against 16.5 us.
+  // One to four rows: dot products, which read each row of A once per channel, where that beats the
+  // tensor cores (us, dot products and tensor cores: 2 x 4096 x 7168 7.4 and 8.6, 2 x 256 x 14336 8.5
+  // and 7.2, 3 x 6144 x 4096 6.8 and 8.3, 3 x 576 x 7168 7.6 and 5.2, 4 x 512 x 4096 3.0 and 3.8,
+  // 4 x 6144 x 4096 9.5 and 8.2).  Two channels per warp for two rows of three blocks per SM or
+  // more: 2 x 7168 x 2048 3.9 against 4.6, 2 x 5120 x 2048 3.3 against 3.1.
   if (M == 1) return launch_i8_gemv<1, 1>(a, lda, w, ldw, p, st);
-  if (M == 2 && N >= 64 * sms) return launch_i8_gemv<2, 2>(a, lda, w, ldw, p, st);
-  if (M == 2) return launch_i8_gemv<2, 1>(a, lda, w, ldw, p, st);
-  if (M == 3 && N < 16 * sms) return launch_i8_gemv<3, 1>(a, lda, w, ldw, p, st);
-  if (M == 4 && N < 16 * sms) return launch_i8_gemv<4, 1>(a, lda, w, ldw, p, st);
+  if (M == 2 && K <= 8192 && N >= 48 * sms) return launch_i8_gemv<2, 2>(a, lda, w, ldw, p, st);
+  if (M == 2 && K <= 8192) return launch_i8_gemv<2, 1>(a, lda, w, ldw, p, st);
+  const bool few_macs = K <= 4096 && static_cast<long long>(N) * K * (M - 1) <= (48LL << 20);
+  if (M == 3 && few_macs) return launch_i8_gemv<3, 1>(a, lda, w, ldw, p, st);
+  if (M == 4 && few_macs) return launch_i8_gemv<4, 1>(a, lda, w, ldw, p, st);
   const long long mt = cdiv(M, 128), pairs = cdiv(M, 256) * cdiv(N, 256);
-  // Two-SM tiles for more than 128 rows where they occupy half the SM pairs (1024 x 2560 x 4096, 40
-  // tiles, 16.4 us against 21.4 with one-SM tiles; 512 x 4096 x 4096, 32 tiles, 15.9 against 14.0)
-  if (M > 128 && pairs >= sms / 4)
-    return launch_i8<I8Cfg<2, 256, false, 6>>(a, M, lda, w, w, N, ldw, p, pairs, MOE_K_LINEAR, st);
-  // more 128 x 128 tiles than SMs (at most 128 rows of very many channels): persistent one-SM tiles
-  if (mt * cdiv(N, 128) > sms)
-    return launch_i8<I8Cfg<1, 128, false, 6>>(a, M, lda, w, w, N, ldw, p, mt * cdiv(N, 128), MOE_K_LINEAR, st);
-  // One round of tiles of 128 x bn over ks parts of K each: of those that fit, the one whose CTAs
-  // load the fewest operand bytes.  Exchanging the parts takes about as long as loading 140 KB does
-  // for 128 x 128 sums, and less for fewer (measured, in parts and in one: 128 x 4096 x 1024 6.7
-  // and 5.4 us, 128 x 4096 x 7168 12.1 and 17.7, 32 x 4096 x 1024 4.4 and 5.1, 8 x 512 x 4096 5.6
-  // and 11.0, 77 x 1031 x 1552 5.3 and 7.2).
-  const int KB = static_cast<int>(cdiv(K, 128)), box = M <= kI8SmallRows ? kI8SmallRows : 128;
+  // More 128 x 128 tiles than SMs: persistent, two-SM tiles for more than 128 rows (where those tiles
+  // fit one round the other kernel is faster: 512 x 4736 x 4096 11.7 us against 16.2, 256 x 9472 x 1024
+  // 6.6 against 9.7)
+  if (mt * cdiv(N, 128) > sms) {
+    if (M > 128) return launch_i8<I8Cfg<2, 256, false, 6>>(a, M, lda, w, w, N, ldw, p, pairs, MOE_K_LINEAR, st);
+    if (cdiv(cdiv(N, 256), sms) * 2 <= cdiv(cdiv(N, 128), sms))
+      return launch_i8<I8Cfg<1, 256, false, 4>>(a, M, lda, w, w, N, ldw, p, cdiv(N, 256), MOE_K_LINEAR, st);
+    return launch_i8<I8Cfg<1, 128, false, 6>>(a, M, lda, w, w, N, ldw, p, cdiv(N, 128), MOE_K_LINEAR, st);
+  }
+  // One round of tiles of 128 x bn over ks parts of K each: the shortest by this estimate in ns,
+  // fitted to 170 shapes of 8 to 512 rows (0.6 % above the best choice, 8 % at most).  A K-block
+  // takes its issue or its bytes, and the longer the more CTAs load; a tile its sums; parts an
+  // exchange.  Clusters of four do not reach all SMs (144 CTAs of them took two rounds).
+  const int KB = static_cast<int>(cdiv(K, 128)), box = M <= 32 ? 32 : (M <= 64 ? 64 : 128);
   int best_bn = 128, best_ks = 1;
-  long long best = -1;
+  float best = -1.f;
   for (int bn = 32; bn <= 128; bn *= 2)
     for (int ks = 1; ks <= 4 && ks * 2 <= KB + 1; ks *= 2) {
-      if (mt * cdiv(N, bn) * ks > sms) continue;
-      const long long cost = static_cast<long long>(box + bn) * 128 * cdiv(KB, ks) +
-                             (ks > 1 ? (10 << 10) + bn * (box == 128 ? 1024LL : 64LL) : 0);
-      if (best < 0 || cost < best) {
+      const long long ctas = mt * cdiv(N, bn) * ks;
+      if (ctas > (ks == 4 ? sms - 20 : sms)) continue;
+      const float rows = box + bn, sums = bn * box;
+      const float issue = 140.f + rows * 0.2f, load = rows * 0.94f;
+      const float cost = cdiv(KB, ks) * ((issue > load ? issue : load) + ctas * rows * 0.001f) + sums / 15.f +
+                         (ks > 1 ? 200.f + sums * 0.19f : 0.f);
+      if (best < 0.f || cost < best) {
         best = cost;
         best_bn = bn;
         best_ks = ks;
       }
     }
-  if (best_ks == 1) {
-    if (best_bn == 32) return launch_i8_split<I8SplitCfg<32, 10, true>>(a, lda, w, ldw, p, 1, st);
-    if (best_bn == 64) return launch_i8_split<I8SplitCfg<64, 8, true>>(a, lda, w, ldw, p, 1, st);
-    return launch_i8_split<I8SplitCfg<128, 6, true>>(a, lda, w, ldw, p, 1, st);
-  }
-  if (best_bn == 32) return launch_i8_split<I8SplitCfg<32, 9, false>>(a, lda, w, ldw, p, best_ks, st);
-  if (best_bn == 64) return launch_i8_split<I8SplitCfg<64, 7, false>>(a, lda, w, ldw, p, best_ks, st);
-  return launch_i8_split<I8SplitCfg<128, 4, false>>(a, lda, w, ldw, p, best_ks, st);
+  if (M <= 32) return launch_i8_split_rows<32>(a, lda, w, ldw, p, best_bn, best_ks, st);
+  if (M <= 64) return launch_i8_split_rows<64>(a, lda, w, ldw, p, best_bn, best_ks, st);
+  return launch_i8_split_rows<128>(a, lda, w, ldw, p, best_bn, best_ks, st);
 }
 
 }  // namespace moe

@@ -241,6 +241,39 @@ struct I8Boxes {
                  "r"(col), "r"(row), "r"(smem_u32(base + i * kI8OutBox))
                  : "memory");
   }
+  // 32 outputs of each of the warp's rows, the first `rows` of which are real, columns col .. col +
+  // n - 1: through the boxes as 32 x 32 words (word c of row r at c ^ r), so that a warp stores along
+  // a row.  For rows that are not whole sectors and for the last columns: element by element from
+  // each lane's own row, 4000 x 3401 x 2048 in bf16 took 155 us, this way 36 (3400 columns: 27).
+  MOE_DEVINL void store_rows(const I8Params& p, int lane, long long row, int rows, int col, const float (&v)[32], int n) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+    float* words = reinterpret_cast<float*>(base);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) words[lane * 32 + (i ^ lane)] = v[i];
+    __syncwarp();
+    const long long at = row * p.ldo + col + lane;
+    if (lane < n) {
+      if (p.out_type == MOE_OUT_FP32) copy_rows(words, lane, rows, static_cast<float*>(p.out) + at, p.ldo);
+      else if (p.out_type == MOE_OUT_BF16) copy_rows(words, lane, rows, static_cast<__nv_bfloat16*>(p.out) + at, p.ldo);
+      else copy_rows(words, lane, rows, static_cast<__half*>(p.out) + at, p.ldo);
+    }
+    __syncwarp();
+  }
+  template <class T>
+  static MOE_DEVINL void copy_rows(const float* words, int lane, int rows, T* out, int64_t ldo) {
+    float x[32];  // all reads before the first store, which they would wait for
+#pragma unroll
+    for (int r = 0; r < 32; ++r) x[r] = words[r * 32 + (lane ^ r)];
+    if (rows >= 32) {
+#pragma unroll
+      for (int r = 0; r < 32; ++r, out += ldo) *out = static_cast<T>(x[r]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 32; ++r, out += ldo)
+        if (r < rows) *out = static_cast<T>(x[r]);
+    }
+  }
   // Two boxes side by side, `width` columns each, that start at (row, col); w0, w1: 16 words of
   // this lane's row.  The second one is left out where it starts past n_cols.
   MOE_DEVINL void store2(const CUtensorMap* m, int lane, int row, int col, int width, int n_cols, const uint32_t* w0,
@@ -351,22 +384,24 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      long long issued = 0;
-      bool ok = true;
-      for (int item = first_item; item < total && ok; item += step) {
-        const I8Tile t = i8_decode<Cfg>(item, NT, p, pref, cnt);
-        const int a_box = i8_box_rows(t.count - t.m0 - 128 * static_cast<int>(rank));
-        uint32_t tx = static_cast<uint32_t>(a_box) * BK + Cfg::B_BYTES;
-        if (PAIR) tx += static_cast<uint32_t>(i8_box_rows(t.count - t.m0 - 128)) * BK + Cfg::B_BYTES;  // (the leader's)
-        const int a_row = static_cast<int>(t.row0) + 128 * static_cast<int>(rank);
-        const int b_row = t.group * p.N + t.n_tile * Cfg::OUT_COLS +
-                          (PAIR && !Cfg::SWIGLU ? static_cast<int>(rank) * Cfg::B_ROWS : 0);
-        const CUtensorMap* mA = a_box == kI8SmallRows ? &tmA32 : &tmA;
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait_bounded(&empty_bar[s], ph ^ 1u, &abort_flag)) { ok = false; break; }
+    // (the whole warp in the loop and one elected lane issuing, as for the MMAs below)
+    int s = 0;
+    uint32_t ph = 0;
+    long long issued = 0;
+    bool ok = true;
+    for (int item = first_item; item < total && ok; item += step) {
+      const I8Tile t = i8_decode<Cfg>(item, NT, p, pref, cnt);
+      const int a_box = i8_box_rows(t.count - t.m0 - 128 * static_cast<int>(rank));
+      uint32_t tx = static_cast<uint32_t>(a_box) * BK + Cfg::B_BYTES;
+      if (PAIR) tx += static_cast<uint32_t>(i8_box_rows(t.count - t.m0 - 128)) * BK + Cfg::B_BYTES;  // (the leader's)
+      const int a_row = static_cast<int>(t.row0) + 128 * static_cast<int>(rank);
+      const int b_row = t.group * p.N + t.n_tile * Cfg::OUT_COLS +
+                        (PAIR && !Cfg::SWIGLU ? static_cast<int>(rank) * Cfg::B_ROWS : 0);
+      const CUtensorMap* mA = a_box == kI8SmallRows ? &tmA32 : &tmA;
+      for (int kb = 0; kb < KB; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty_bar[s], ph ^ 1u, &abort_flag));
+        if (!ok) break;
+        if (elect_one()) {
           uint8_t* sa = smem + s * Cfg::STAGE_BYTES;
           uint8_t* sb = sa + Cfg::A_BYTES;
           if constexpr (PAIR) {
@@ -380,22 +415,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             tma_load_2d(sb, &tmB0, kb * BK, b_row, &full_bar[s]);
             if constexpr (Cfg::SWIGLU) tma_load_2d(sb + Cfg::B_BYTES / 2, &tmB1, kb * BK, b_row, &full_bar[s]);
           }
-          ++issued;
-          if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
+        __syncwarp();
+        ++issued;
+        if (++s == STAGES) { s = 0; ph ^= 1u; }
       }
-      if (leader) {
-        // (the leader's stage barriers count the peer's bytes too)
-        volatile int* no_abort = &no_abort_sh[0];
-        const long long back = issued < STAGES ? issued : STAGES;
-        for (long long j = 0; j < back; ++j) {
-          if (s == 0) { s = STAGES - 1; ph ^= 1u; } else { --s; }
-          mbar_wait_bounded(&full_bar[s], ph, no_abort);
-        }
-        if (*no_abort) abort_flag = 1;
-      }
-      if (!ok) abort_flag = 1;
     }
+    if (leader) {
+      // (the leader's stage barriers count the peer's bytes too)
+      volatile int* no_abort = &no_abort_sh[0];
+      const long long back = issued < STAGES ? issued : STAGES;
+      for (long long j = 0; j < back; ++j) {
+        if (s == 0) { s = STAGES - 1; ph ^= 1u; } else { --s; }
+        mbar_wait_bounded(&full_bar[s], ph, no_abort);
+      }
+      if (*no_abort) abort_flag = 1;
+    }
+    if (!ok) abort_flag = 1;
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA (the leader's)
     // The whole warp runs the loop and one elected lane issues: what an MMA takes stays in
@@ -446,6 +482,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const int q = warp & 3;  // TMEM lane quadrant
     float* cols = col_sh[q];
     I8Boxes out_boxes{smem + STAGES * Cfg::STAGE_BYTES + q * 2 * kI8OutBox};
+    // a row's 32 outputs are whole 32-byte sectors
+    const bool whole = ((reinterpret_cast<uintptr_t>(p.out) |
+                         static_cast<uintptr_t>(p.ldo * (Cfg::SWIGLU || p.out_type == MOE_OUT_FP32 ? 4 : 2))) & 31) == 0;
     const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&tempty_bar[0]), 0) : 0u;
     const uint32_t tempty1 = PAIR ? mapa_shared(smem_u32(&tempty_bar[1]), 0) : 0u;
     int acc = 0;
@@ -473,6 +512,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       // a warp's 32 rows go out in boxes where all of them are real, else row by row
       const bool boxes = p.tma_store && t.m0 + 128 * static_cast<int>(rank) + q * 32 + 32 <= t.count;
       const int box_row = static_cast<int>(t.row0) + 128 * static_cast<int>(rank) + q * 32;
+      const int rows_here = t.count - t.m0 - 128 * static_cast<int>(rank) - q * 32;  // 32 or more: all
       if constexpr (Cfg::SWIGLU) {
         float* out = static_cast<float*>(p.out) + row * p.ldo + col0;
 #pragma unroll 1
@@ -524,8 +564,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               if (boxes)
                 out_boxes.store2(&tmOut, lane, box_row, col, 16, p.N, reinterpret_cast<const uint32_t*>(v),
                                  reinterpret_cast<const uint32_t*>(v) + 16);
-              else if (row_ok)
-                i8_store32(p, row, col, v, p.N - col);
+              else if (whole && p.N - col >= 32) {
+                if (row_ok) i8_store32(p, row, col, v, 32);
+              } else if (rows_here > 0) {
+                out_boxes.store_rows(p, lane, row - lane, rows_here, col, v, p.N - col);
+              }
             }
           }
         }
@@ -559,22 +602,29 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 // their s32 sums of those columns into its shared memory (posted stores, nothing waits for a
 // round trip), and after one cluster barrier it adds the KS parts (any order gives the same
 // integer), scales and stores them.  No workspace, no atomics, one launch.
-// Measured on B200, 128 x 7168 x 4096: reading the parts from the peers instead of having them
-// pushed cost 5 us more.
+// What bounds it: HBM for long weights, else the K-loop's steps and the exchange.  Measured on B200:
+// reading the parts from the peers instead of having them pushed 18.1 us against 15.4 (128 x 7168 x
+// 4096); loads issued by one lane in the loop 0.24 us a step, by an elected lane of the whole warp
+// 0.18, and with two K-blocks per step 0.14 a block (512 x 4096, 8 rows, one part: 10.5, 8.7, 6.9 us).
 // LONE: one part, whose sums may go into the stage ring (others' could arrive while it is in use).
-template <int BN_, int STAGES_, bool LONE_>
+template <int BN_, int ROWS_, int SUB_, int STAGES_, bool LONE_>
 struct I8SplitCfg {
   static constexpr int BN = BN_;
+  static constexpr int ROWS = ROWS_;             // rows of A loaded (the MMA reads 128: what lies behind)
+  static constexpr int SUB = SUB_;               // K-blocks of 128 per stage
   static constexpr int STAGES = STAGES_;
   static constexpr int BK = 128;
-  static constexpr int A_BYTES = 128 * BK;
-  static constexpr int STAGE_BYTES = A_BYTES + BN * BK;
+  static constexpr int A_BYTES = ROWS * BK;      // per K-block
+  static constexpr int B_BYTES = BN * BK;
+  static constexpr int RING_BYTES = STAGES * SUB * (A_BYTES + B_BYTES);  // all of A's blocks, then all of B's
   // received parts: [part][column group of 4][row ^ (group & 7)] int4: a warp's push (a lane per
   // row) is 512 contiguous bytes, and lanes that read along a row meet no bank twice
-  static constexpr int PART_BYTES = 128 * BN * 4;
+  static constexpr int GROUP_BYTES = ROWS * 16;
+  static constexpr int PART_BYTES = ROWS * BN * 4;
   static constexpr bool LONE = LONE_;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + (LONE ? 0 : PART_BYTES) + 1024;
-  static_assert(PART_BYTES <= STAGES * STAGE_BYTES, "the sums fit the ring");
+  static constexpr int SMEM_BYTES = RING_BYTES + (LONE ? 0 : PART_BYTES) + 1024;
+  static_assert(PART_BYTES <= RING_BYTES, "the sums fit the ring");
+  static_assert(STAGES * SUB * B_BYTES >= 128 * BK - A_BYTES, "what the MMA reads behind A is in the ring");
   static constexpr int TMEM_COLS = BN;
   static constexpr int THREADS = 192;
   static_assert(SMEM_BYTES + 2 * BN * 4 + 2048 <= 227 * 1024, "shared memory");
@@ -591,7 +641,7 @@ MOE_DEVINL void st_cluster_v4(uint32_t addr, const uint32_t* v) {
 // (128 / groups)th row.  KS and the output type are fixed at compile time: a CTA has one such warp
 // per scheduler, so the stage takes as long as its instructions (with them in registers, and four
 // rows at a time, 1 us instead of 3).
-template <int KS, int TYPE>
+template <int KS, int TYPE, int GROUP_BYTES>
 MOE_DEVINL void i8_finish_parts(const I8Params& p, const uint8_t* parts, int t, int log_groups, int m0, int rows, int col,
                                 const float* scale, const float* bias, const float* row_scale) {
   using Word = typename std::conditional<TYPE == MOE_OUT_FP32, float4, uint2>::type;
@@ -604,8 +654,8 @@ MOE_DEVINL void i8_finish_parts(const I8Params& p, const uint8_t* parts, int t, 
   uint8_t* out = static_cast<uint8_t*>(p.out) + (m0 * p.ldo + col) * ESZ;
   const int64_t pitch = p.ldo * ESZ;
   const bool vec = p.N - col >= 4 && ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(pitch)) & (sizeof(Word) - 1)) == 0;
-  const uint8_t* at = parts + g * 2048;
-  const int part_bytes = groups * 2048, swz = g & 7;
+  const uint8_t* at = parts + g * GROUP_BYTES;
+  const int part_bytes = groups * GROUP_BYTES, swz = g & 7;
 #pragma unroll 4
   for (int r = t >> log_groups; r < rows; r += 128 >> log_groups) {
     int4 a[KS];
@@ -644,8 +694,8 @@ MOE_DEVINL void i8_finish_parts(const I8Params& p, const uint8_t* parts, int t, 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tc_gemm_i8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                            const int a_box, const I8Params p) {
-  constexpr int BN = Cfg::BN, BK = Cfg::BK, STAGES = Cfg::STAGES;
+                            const I8Params p) {
+  constexpr int BN = Cfg::BN, BK = Cfg::BK, SUB = Cfg::SUB, STAGES = Cfg::STAGES;
   constexpr uint32_t IDESC = idesc_i8_s32(128, BN);
   extern __shared__ uint8_t dsmem[];
   __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES], done_bar;
@@ -656,11 +706,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   const int warp = warp_id(), lane = lane_id();
   const uint32_t pad = (1024u - (smem_u32(dsmem) & 1023u)) & 1023u;
   uint8_t* smem = dsmem + pad;
-  uint8_t* parts = smem + (Cfg::LONE ? 0 : STAGES * Cfg::STAGE_BYTES);
+  uint8_t* ring_b = smem + STAGES * SUB * Cfg::A_BYTES;
+  uint8_t* parts = smem + (Cfg::LONE ? 0 : Cfg::RING_BYTES);
   const int ks = Cfg::LONE ? 1 : gridDim.x, part = blockIdx.x;  // the cluster spans the grid's x
-  const int KB = (p.K + BK - 1) / BK;
-  int kb0, kb1;
-  k_slice(part, ks, KB, kb0, kb1);
+  const int steps = (p.K + SUB * BK - 1) / (SUB * BK);
+  int step0, step1;
+  k_slice(part, ks, steps, step0, step1);
   const int m0 = blockIdx.z * 128, col0 = blockIdx.y * BN;
 
   if (threadIdx.x == 0) {
@@ -690,40 +741,47 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   pdl_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      int issued = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(&empty_bar[s], ph ^ 1u, &abort_flag)) break;
-        uint8_t* sa = smem + s * Cfg::STAGE_BYTES;
-        mbar_arrive_expect_tx(&full_bar[s], static_cast<uint32_t>((a_box + BN) * BK));
-        tma_load_2d(sa, &tmA, kb * BK, m0, &full_bar[s]);
-        tma_load_2d(sa + Cfg::A_BYTES, &tmB, kb * BK, col0, &full_bar[s]);
-        ++issued;
-        if (++s == STAGES) { s = 0; ph ^= 1u; }
-      }
-      volatile int no_abort = 0;
-      const int back = issued < STAGES ? issued : STAGES;
-      for (int j = 0; j < back; ++j) {
-        if (s == 0) { s = STAGES - 1; ph ^= 1u; } else { --s; }
-        mbar_wait_bounded(&full_bar[s], ph, &no_abort);
-      }
-      if (no_abort) abort_flag = 1;
-    }
-  } else if (warp == 1) {
     // (the whole warp in the loop, one lane issues: see tc_gemm_i8_kernel)
     int s = 0;
     uint32_t ph = 0;
-    const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
-    for (int kb = kb0; kb < kb1; ++kb) {
+    int issued = 0;
+    for (int step = step0; step < step1; ++step) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty_bar[s], ph ^ 1u, &abort_flag))) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&full_bar[s], SUB * (Cfg::A_BYTES + Cfg::B_BYTES));
+#pragma unroll
+        for (int j = 0; j < SUB; ++j) {  // (past K: zeros)
+          tma_load_2d(smem + (s * SUB + j) * Cfg::A_BYTES, &tmA, (step * SUB + j) * BK, m0, &full_bar[s]);
+          tma_load_2d(ring_b + (s * SUB + j) * Cfg::B_BYTES, &tmB, (step * SUB + j) * BK, col0, &full_bar[s]);
+        }
+      }
+      __syncwarp();
+      ++issued;
+      if (++s == STAGES) { s = 0; ph ^= 1u; }
+    }
+    volatile int no_abort = 0;
+    const int back = issued < STAGES ? issued : STAGES;
+    for (int j = 0; j < back; ++j) {
+      if (s == 0) { s = STAGES - 1; ph ^= 1u; } else { --s; }
+      mbar_wait_bounded(&full_bar[s], ph, &no_abort);
+    }
+    if (no_abort) abort_flag = 1;
+  } else if (warp == 1) {
+    int s = 0;
+    uint32_t ph = 0;
+    const uint64_t desc_a = smem_desc_sw128(smem_u32(smem)), desc_b = smem_desc_sw128(smem_u32(ring_b));
+    for (int step = step0; step < step1; ++step) {
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full_bar[s], ph, &abort_flag))) break;
       tc_fence_after();
-      const uint64_t da = desc0 + static_cast<uint32_t>(s * (Cfg::STAGE_BYTES >> 4));
-      const uint64_t db = da + (Cfg::A_BYTES >> 4);
+      const uint64_t da = desc_a + static_cast<uint32_t>(s * SUB * (Cfg::A_BYTES >> 4));
+      const uint64_t db = desc_b + static_cast<uint32_t>(s * SUB * (Cfg::B_BYTES >> 4));
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < BK / 32; ++k) umma_i8<1>(tmem_base, da + 2 * k, db + 2 * k, IDESC, kb != kb0 || k != 0);
+        for (int j = 0; j < SUB; ++j)
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)
+            umma_i8<1>(tmem_base, da + j * (Cfg::A_BYTES >> 4) + 2 * k, db + j * (Cfg::B_BYTES >> 4) + 2 * k, IDESC,
+                       step != step0 || (j | k) != 0);
         umma_commit(&empty_bar[s]);
       }
       __syncwarp();
@@ -775,7 +833,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       }
     }
   } else if (warp >= 2 && m0 + q * 32 < p.dense_rows) {
-    const uint32_t mine = smem_u32(parts) + part * groups * 2048;
+    const uint32_t mine = smem_u32(parts) + part * groups * Cfg::GROUP_BYTES;
 #pragma unroll 1
     for (int c = 0; c < BN; c += 32) {
       uint32_t r[32];
@@ -784,7 +842,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
         const int g = ((c + i) >> 2) & (groups - 1);
-        const uint32_t to = mine + g * 2048 + ((row ^ (g & 7)) << 4);
+        const uint32_t to = mine + g * Cfg::GROUP_BYTES + ((row ^ (g & 7)) << 4);
         st_cluster_v4(ks > 1 ? mapa_shared(to, (c + i) >> (log_groups + 2)) : to, r + i);
       }
     }
@@ -797,11 +855,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     auto finish = [&](auto ks_c) {
       constexpr int KS = decltype(ks_c)::value;
       if (p.out_type == MOE_OUT_BF16)
-        i8_finish_parts<KS, MOE_OUT_BF16>(p, parts, t, log_groups, m0, rows, col0 + first, scale_sh + first, bias_sh + first, row_sh);
+        i8_finish_parts<KS, MOE_OUT_BF16, Cfg::GROUP_BYTES>(p, parts, t, log_groups, m0, rows, col0 + first, scale_sh + first, bias_sh + first, row_sh);
       else if (p.out_type == MOE_OUT_FP16)
-        i8_finish_parts<KS, MOE_OUT_FP16>(p, parts, t, log_groups, m0, rows, col0 + first, scale_sh + first, bias_sh + first, row_sh);
+        i8_finish_parts<KS, MOE_OUT_FP16, Cfg::GROUP_BYTES>(p, parts, t, log_groups, m0, rows, col0 + first, scale_sh + first, bias_sh + first, row_sh);
       else
-        i8_finish_parts<KS, MOE_OUT_FP32>(p, parts, t, log_groups, m0, rows, col0 + first, scale_sh + first, bias_sh + first, row_sh);
+        i8_finish_parts<KS, MOE_OUT_FP32, Cfg::GROUP_BYTES>(p, parts, t, log_groups, m0, rows, col0 + first, scale_sh + first, bias_sh + first, row_sh);
     };
     if constexpr (Cfg::LONE) finish(std::integral_constant<int, 1>());
     else if (ks == 2) finish(std::integral_constant<int, 2>());

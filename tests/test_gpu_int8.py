@@ -75,6 +75,25 @@ def test_linear_few_rows(M, N, K, dtype):
     check_linear(args, ref, tol)
 
 
+# Shapes for which the launch rule (on 148 SMs) takes each tile width, number of A rows and number
+# of parts; the first three have one to four rows on either side of the dot products' limit.
+TILES = [(2, 256, 8208), (3, 301, 4112), (4, 4200, 2048),
+         (5, 16, 32), (6, 17, 704), (7, 19, 800), (33, 16, 32), (37, 1096, 912), (34, 17, 896),
+         (66, 16, 32), (130, 606, 1520), (68, 18, 976),
+         (5, 4826, 32), (9, 2645, 1168), (32, 1064, 784), (35, 5155, 32), (37, 2399, 1968), (64, 1052, 1808),
+         (142, 2378, 32), (65, 2393, 3344), (67, 1048, 3536),
+         (5, 9484, 32), (13, 4969, 2000), (31, 2471, 1840), (33, 9890, 32), (35, 5156, 3552), (63, 2514, 3728),
+         (129, 4819, 32), (67, 4753, 7984), (127, 2776, 7952), (120, 19001, 144), (16, 38100, 64)]
+
+
+@pytest.mark.parametrize("M,N,K", TILES)
+def test_linear_tiles(M, N, K):
+    for i, dtype in enumerate(KIND):
+        args, ref, tol = linear_case(M, N, K, dtype, bias=i == 1, pad=(0, 16, (0, 1, 8)[(M + i) % 3]), seed=M + i)
+        linear(*args)
+        check_linear(args, ref, tol)
+
+
 @pytest.mark.parametrize("M", [1, 3, 20, 200])
 def test_linear_longest_sum(M):
     """K = 131056 with every code -128: the sum 2147221504 is the largest that 32 bits hold here."""
