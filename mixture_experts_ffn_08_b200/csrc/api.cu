@@ -415,14 +415,18 @@ moe_status_t do_expert_ffn_i8(const moe_params_t* p, const void* x_perm, const f
   // tiles) 34 against 26.  (The kernels take the schedule from the counts, in both layouts.)
   const long long P = static_cast<long long>(p->T) * p->K;
   const bool tall = P >= 160LL * p->E;
+  const long long m_tiles = P / kBlockM + (P < p->E ? P : p->E);  // at most
+  const int rows = static_cast<int>(P / p->E < kBlockM ? P / p->E : kBlockM);
   const bool pair_gu = tall && P / 256 * (p->I / 128) >= num_sms();
   const bool pair_dn = tall && P / 256 * ((p->H + 255) / 256) >= num_sms();
+  const int tile_gu = pair_gu ? kI8PairTile : i8_tile_width(m_tiles, rows, 2LL * p->I);
+  const int tile_dn = pair_dn ? kI8PairTile : i8_tile_width(m_tiles, rows, p->H);
   const I8Rows x{x_perm, x_perm_scale, L.max_rows, offsets, counts, p->E, p->masked_cap};
   const I8Rows hq{at<void>(ws, L.hq), at<float>(ws, L.hq_scale), L.max_rows, offsets, counts, p->E, p->masked_cap};
-  MOE_CUDA(gemm_i8_gateup_swiglu(x, w_gate, w_up, gate_scale, up_scale, p->I, p->H, h, status, pair_gu, st));
+  MOE_CUDA(gemm_i8_gateup_swiglu(x, w_gate, w_up, gate_scale, up_scale, p->I, p->H, h, status, tile_gu, st));
   MOE_CUDA(launch_quant_rows(h, L.max_rows, offsets, counts, p->E, p->masked_cap, p->I, at<void>(ws, L.hq),
                              at<float>(ws, L.hq_scale), st));
-  MOE_CUDA(gemm_i8_down(hq, w_down, down_scale, p->H, p->I, y_perm, status, pair_dn, st));
+  MOE_CUDA(gemm_i8_down(hq, w_down, down_scale, p->H, p->I, y_perm, status, tile_dn, st));
   return MOE_OK;
 }
 

@@ -74,7 +74,7 @@ cudaError_t allow_smem(Kern kern, int bytes, std::atomic<unsigned long long>& do
 template <class Cfg>
 cudaError_t launch_i8(const void* A, int64_t a_rows, int64_t lda, const void* b0, const void* b1, int64_t b_rows,
                       int64_t ldb, I8Params p, long long max_items, int kid, cudaStream_t st) {
-  constexpr uint32_t b_box = Cfg::SWIGLU ? 128 : Cfg::B_ROWS;
+  constexpr uint32_t b_box = Cfg::SWIGLU ? Cfg::BN / 2 : Cfg::B_ROWS;
   CUtensorMap ta, ta32, tb0, tb1;
   if (!make_tmap_i8(&ta, A, a_rows, p.K, lda, 128) || !make_tmap_i8(&ta32, A, a_rows, p.K, lda, kI8SmallRows) ||
       !make_tmap_i8(&tb0, b0, b_rows, p.K, ldb, b_box))
@@ -391,8 +391,27 @@ cudaError_t launch_quant_rows(const float* h, long long max_rows, const int32_t*
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
+// Rounds of tiles times the ns that a K-block of one takes (as in gemm_i8_linear).  One token through
+// two of eight experts of 4096 x 14336: 75 us, 94 with tiles of 256 alone; 33 tokens through eight of
+// 256 x 128: 10.5 us against 13.6.  A batch that fills the SMs many times keeps the widest tiles, which
+// read the rows of A least often.
+int i8_tile_width(long long m_tiles, int tile_rows, long long rows) {
+  const long long sms = num_sms();
+  int best_bn = 256;
+  float best = -1.f;
+  for (int bn = 256; bn >= 64; bn /= 2) {
+    const float r = (tile_rows <= kI8SmallRows ? kI8SmallRows : 128) + bn, issue = 140.f + r * 0.2f, load = r * 0.94f;
+    const float cost = cdiv(m_tiles * cdiv(rows, bn), sms) * (issue > load ? issue : load);
+    if (best < 0.f || cost < best) {
+      best = cost;
+      best_bn = bn;
+    }
+  }
+  return best_bn;
+}
+
 cudaError_t gemm_i8_gateup_swiglu(const I8Rows& a, const void* w_gate, const void* w_up, const float* gate_scale,
-                                  const float* up_scale, int N, int K, float* h, int32_t* status, bool pair,
+                                  const float* up_scale, int N, int K, float* h, int32_t* status, int tile,
                                   cudaStream_t st) {
   I8Params p{};
   p.offsets = a.offsets;
@@ -408,14 +427,18 @@ cudaError_t gemm_i8_gateup_swiglu(const I8Rows& a, const void* w_gate, const voi
   p.ldo = N;
   p.status = status;
   const int64_t b_rows = static_cast<int64_t>(a.G) * N;
-  const long long items = cdiv(a.rows, 128) * cdiv(N, 128);
-  if (pair)
-    return launch_i8<I8Cfg<2, 256, true, 6>>(a.codes, a.rows, K, w_gate, w_up, b_rows, K, p, items, MOE_K_GATEUP, st);
-  return launch_i8<I8Cfg<1, 256, true, 4>>(a.codes, a.rows, K, w_gate, w_up, b_rows, K, p, items, MOE_K_GATEUP, st);
+  const long long mt = cdiv(a.rows, 128);
+  if (tile == kI8PairTile)
+    return launch_i8<I8Cfg<2, 256, true, 6>>(a.codes, a.rows, K, w_gate, w_up, b_rows, K, p, mt * cdiv(N, 128), MOE_K_GATEUP, st);
+  if (tile == 256)
+    return launch_i8<I8Cfg<1, 256, true, 4>>(a.codes, a.rows, K, w_gate, w_up, b_rows, K, p, mt * cdiv(N, 128), MOE_K_GATEUP, st);
+  if (tile == 128)
+    return launch_i8<I8Cfg<1, 128, true, 3, 2>>(a.codes, a.rows, K, w_gate, w_up, b_rows, K, p, mt * cdiv(N, 64), MOE_K_GATEUP, st);
+  return launch_i8<I8Cfg<1, 64, true, 4, 2>>(a.codes, a.rows, K, w_gate, w_up, b_rows, K, p, mt * cdiv(N, 32), MOE_K_GATEUP, st);
 }
 
 cudaError_t gemm_i8_down(const I8Rows& a, const void* w, const float* w_scale, int N, int K, void* y, int32_t* status,
-                         bool pair, cudaStream_t st) {
+                         int tile, cudaStream_t st) {
   I8Params p{};
   p.offsets = a.offsets;
   p.counts = a.counts;
@@ -430,10 +453,14 @@ cudaError_t gemm_i8_down(const I8Rows& a, const void* w, const float* w_scale, i
   p.ldo = N;
   p.status = status;
   const int64_t b_rows = static_cast<int64_t>(a.G) * N;
-  const long long items = cdiv(a.rows, 128) * cdiv(N, 256);
-  if (pair)
-    return launch_i8<I8Cfg<2, 256, false, 6>>(a.codes, a.rows, K, w, w, b_rows, K, p, items, MOE_K_DOWN, st);
-  return launch_i8<I8Cfg<1, 256, false, 4>>(a.codes, a.rows, K, w, w, b_rows, K, p, items, MOE_K_DOWN, st);
+  const long long mt = cdiv(a.rows, 128);
+  if (tile == kI8PairTile)
+    return launch_i8<I8Cfg<2, 256, false, 6>>(a.codes, a.rows, K, w, w, b_rows, K, p, mt * cdiv(N, 256), MOE_K_DOWN, st);
+  if (tile == 256)
+    return launch_i8<I8Cfg<1, 256, false, 4>>(a.codes, a.rows, K, w, w, b_rows, K, p, mt * cdiv(N, 256), MOE_K_DOWN, st);
+  if (tile == 128)
+    return launch_i8<I8Cfg<1, 128, false, 3, 2>>(a.codes, a.rows, K, w, w, b_rows, K, p, mt * cdiv(N, 128), MOE_K_DOWN, st);
+  return launch_i8<I8Cfg<1, 64, false, 4, 2>>(a.codes, a.rows, K, w, w, b_rows, K, p, mt * cdiv(N, 64), MOE_K_DOWN, st);
 }
 
 cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, const float* a_scale, const void* w,
@@ -471,7 +498,7 @@ cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, cons
     if (M > 128) return launch_i8<I8Cfg<2, 256, false, 6>>(a, M, lda, w, w, N, ldw, p, pairs, MOE_K_LINEAR, st);
     if (cdiv(cdiv(N, 256), sms) * 2 <= cdiv(cdiv(N, 128), sms))
       return launch_i8<I8Cfg<1, 256, false, 4>>(a, M, lda, w, w, N, ldw, p, cdiv(N, 256), MOE_K_LINEAR, st);
-    return launch_i8<I8Cfg<1, 128, false, 6>>(a, M, lda, w, w, N, ldw, p, cdiv(N, 128), MOE_K_LINEAR, st);
+    return launch_i8<I8Cfg<1, 128, false, 3, 2>>(a, M, lda, w, w, N, ldw, p, cdiv(N, 128), MOE_K_LINEAR, st);
   }
   // One round of tiles of 128 x bn over ks parts of K each: the shortest by this estimate in ns,
   // fitted to 170 shapes of 8 to 512 rows (0.6 % above the best choice, 8 % at most).  A K-block

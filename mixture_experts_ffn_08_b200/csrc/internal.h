@@ -196,15 +196,19 @@ struct I8Rows {
   int masked_cap;
 };
 // h [rows, N] fp32 = SiLU(A Wg^T) * (A Wu^T) on the real rows.  pair: tiles of two CTAs.
+// Width of a one-SM tile for m_tiles tiles of about tile_rows rows by `rows` weight rows (both of gate
+// and up): the narrower ones where the wide ones leave SMs idle.
+int i8_tile_width(long long m_tiles, int tile_rows, long long rows);
+constexpr int kI8PairTile = 0;  // `tile` below: 256 x 256 over two SMs, else a width
 cudaError_t gemm_i8_gateup_swiglu(const I8Rows& a, const void* w_gate, const void* w_up, const float* gate_scale,
-                                  const float* up_scale, int N, int K, float* h, int32_t* status, bool pair,
+                                  const float* up_scale, int N, int K, float* h, int32_t* status, int tile,
                                   cudaStream_t st);
 // h's real rows as int8 codes with one scale per row.
 cudaError_t launch_quant_rows(const float* h, long long max_rows, const int32_t* offsets, const int32_t* counts, int E,
                               int cap, int cols, void* codes, float* scale, cudaStream_t st);
 // y [rows, N] bf16 = A W^T on the real rows.
 cudaError_t gemm_i8_down(const I8Rows& a, const void* w, const float* w_scale, int N, int K, void* y, int32_t* status,
-                         bool pair, cudaStream_t st);
+                         int tile, cudaStream_t st);
 // out [M, N] (row stride ldo) = A W^T + bias.
 cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, const float* a_scale, const void* w,
                            int64_t ldw, const float* w_scale, const float* bias, int out_type, void* out, int64_t ldo,

@@ -81,17 +81,19 @@ MOE_DEVINL void umma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_
         : "memory");
 }
 
-template <int CG_, int BN_, bool SWIGLU_, int STAGES_>
+template <int CG_, int BN_, bool SWIGLU_, int STAGES_, int SUB_ = 1>
 struct I8Cfg {
   static constexpr int CG = CG_;
   static constexpr int BN = BN_;
   static constexpr bool SWIGLU = SWIGLU_;
   static constexpr int STAGES = STAGES_;
-  static constexpr int BK = 128;                 // codes per K-step: one 128-byte swizzle row
+  static constexpr int SUB = SUB_;               // K-blocks per stage
+  static constexpr int BK = 128;                 // codes per K-block: one 128-byte swizzle row
   static constexpr int A_BYTES = 128 * BK;
   static constexpr int B_ROWS = BN / CG;         // B rows held by each CTA
   static constexpr int B_BYTES = B_ROWS * BK;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int BLOCK_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGE_BYTES = SUB * BLOCK_BYTES;
   static constexpr int OUT_BYTES = 4 * 2 * kI8OutBox;  // two boxes per epilogue warp
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + 1024;
   static constexpr int OUT_COLS = SWIGLU ? BN / 2 : BN;
@@ -99,7 +101,7 @@ struct I8Cfg {
   static constexpr int TILE_M = 128 * CG;
   static constexpr int THREADS = 192;
   static_assert(BN == 32 || BN == 64 || BN == 128 || BN == 256, "two accumulators in a power of two of TMEM columns");
-  static_assert(!SWIGLU || BN == 256, "a SwiGLU tile is 128 gate and 128 up rows");
+  static_assert(!SWIGLU || BN >= 64, "a SwiGLU tile is half gate and half up rows");
   static_assert(CG == 1 || BN == 256, "pair tiles are 256 x 256");
   static_assert(SMEM_BYTES + 8 * (kI8MaxGroups + 1) + 4 * 512 * 4 + 512 <= 227 * 1024, "shared memory");
 };
@@ -294,13 +296,13 @@ struct I8Boxes {
 };
 
 // tmA: boxes of 128 rows of A, tmA32: of 32.  tmB0 (and tmB1, the up weights of SWIGLU): boxes
-// of B_ROWS rows, or of 128 for SWIGLU.  tmOut (with p.tma_store): boxes of 32 rows x 64 bytes.
+// of B_ROWS rows, or of BN / 2 for SWIGLU.  tmOut (with p.tma_store): boxes of 32 rows x 64 bytes.
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tc_gemm_i8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
                       const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
                       const __grid_constant__ CUtensorMap tmOut, const I8Params p) {
-  constexpr int CG = Cfg::CG, BN = Cfg::BN, BK = Cfg::BK, STAGES = Cfg::STAGES;
+  constexpr int CG = Cfg::CG, BN = Cfg::BN, BK = Cfg::BK, SUB = Cfg::SUB, STAGES = Cfg::STAGES;
   constexpr bool PAIR = CG == 2;
   constexpr uint32_t IDESC = idesc_i8_s32(Cfg::TILE_M, BN);
 
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   const uint32_t pad = (1024u - (smem_u32(dsmem) & 1023u)) & 1023u;
   uint8_t* smem = dsmem + pad;
   const int NT = (p.N + Cfg::OUT_COLS - 1) / Cfg::OUT_COLS;
-  const int KB = (p.K + BK - 1) / BK;
+  const int KB = (p.K + SUB * BK - 1) / (SUB * BK);  // stages' worth
   const int first_item = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (threadIdx.x == 0) {
@@ -392,8 +394,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     for (int item = first_item; item < total && ok; item += step) {
       const I8Tile t = i8_decode<Cfg>(item, NT, p, pref, cnt);
       const int a_box = i8_box_rows(t.count - t.m0 - 128 * static_cast<int>(rank));
-      uint32_t tx = static_cast<uint32_t>(a_box) * BK + Cfg::B_BYTES;
-      if (PAIR) tx += static_cast<uint32_t>(i8_box_rows(t.count - t.m0 - 128)) * BK + Cfg::B_BYTES;  // (the leader's)
+      uint32_t tx = SUB * (static_cast<uint32_t>(a_box) * BK + Cfg::B_BYTES);
+      if (PAIR) tx += SUB * (static_cast<uint32_t>(i8_box_rows(t.count - t.m0 - 128)) * BK + Cfg::B_BYTES);  // (the leader's)
       const int a_row = static_cast<int>(t.row0) + 128 * static_cast<int>(rank);
       const int b_row = t.group * p.N + t.n_tile * Cfg::OUT_COLS +
                         (PAIR && !Cfg::SWIGLU ? static_cast<int>(rank) * Cfg::B_ROWS : 0);
@@ -402,18 +404,25 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty_bar[s], ph ^ 1u, &abort_flag));
         if (!ok) break;
         if (elect_one()) {
-          uint8_t* sa = smem + s * Cfg::STAGE_BYTES;
-          uint8_t* sb = sa + Cfg::A_BYTES;
           if constexpr (PAIR) {
-            const uint32_t bar = mapa_shared(smem_u32(&full_bar[s]), 0);
             if (leader) mbar_arrive_expect_tx(&full_bar[s], tx);
-            if (a_box > 0) tma_load_2d_pair(sa, mA, kb * BK, a_row, bar);
-            tma_load_2d_pair(sb, (Cfg::SWIGLU && rank == 1) ? &tmB1 : &tmB0, kb * BK, b_row, bar);
           } else {
             mbar_arrive_expect_tx(&full_bar[s], tx);
-            tma_load_2d(sa, mA, kb * BK, a_row, &full_bar[s]);
-            tma_load_2d(sb, &tmB0, kb * BK, b_row, &full_bar[s]);
-            if constexpr (Cfg::SWIGLU) tma_load_2d(sb + Cfg::B_BYTES / 2, &tmB1, kb * BK, b_row, &full_bar[s]);
+          }
+#pragma unroll
+          for (int j = 0; j < SUB; ++j) {  // (past K: zeros)
+            uint8_t* sa = smem + s * Cfg::STAGE_BYTES + j * Cfg::BLOCK_BYTES;
+            uint8_t* sb = sa + Cfg::A_BYTES;
+            const int k = (kb * SUB + j) * BK;
+            if constexpr (PAIR) {
+              const uint32_t bar = mapa_shared(smem_u32(&full_bar[s]), 0);
+              if (a_box > 0) tma_load_2d_pair(sa, mA, k, a_row, bar);
+              tma_load_2d_pair(sb, (Cfg::SWIGLU && rank == 1) ? &tmB1 : &tmB0, k, b_row, bar);
+            } else {
+              tma_load_2d(sa, mA, k, a_row, &full_bar[s]);
+              tma_load_2d(sb, &tmB0, k, b_row, &full_bar[s]);
+              if constexpr (Cfg::SWIGLU) tma_load_2d(sb + Cfg::B_BYTES / 2, &tmB1, k, b_row, &full_bar[s]);
+            }
           }
         }
         __syncwarp();
@@ -456,7 +465,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           const uint64_t db = da + (Cfg::A_BYTES >> 4);
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < BK / 32; ++k) umma_i8<CG>(d_tmem, da + 2 * k, db + 2 * k, IDESC, (kb | k) != 0);
+            for (int j = 0; j < SUB; ++j)
+#pragma unroll
+              for (int k = 0; k < BK / 32; ++k)
+                umma_i8<CG>(d_tmem, da + j * (Cfg::BLOCK_BYTES >> 4) + 2 * k, db + j * (Cfg::BLOCK_BYTES >> 4) + 2 * k, IDESC,
+                            (kb | j | k) != 0);
             if constexpr (PAIR) umma_commit_pair(&empty_bar[s]); else umma_commit(&empty_bar[s]);
           }
           __syncwarp();
@@ -516,10 +529,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       if constexpr (Cfg::SWIGLU) {
         float* out = static_cast<float*>(p.out) + row * p.ldo + col0;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < Cfg::OUT_COLS; c += 32) {
           uint32_t rg[32], ru[32];
           tmem_ld_32x32b_x32(tbase + c, rg);
-          tmem_ld_32x32b_x32(tbase + 128 + c, ru);
+          tmem_ld_32x32b_x32(tbase + BN / 2 + c, ru);
           tmem_ld_wait(rg);
           reg_fence(ru);
           float g[32], u[32];

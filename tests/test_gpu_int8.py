@@ -238,6 +238,7 @@ def skewed_ids(wl, seed, empty=0):
     (2000, 2560, 1280, 5, 2, 0, 1),   # enough tiles for pairs of CTAs in both products
     (2000, 2560, 1280, 5, 2, 2048, 0),
     (1500, 256, 256, 5, 3, 0, 2), (300, 1152, 128, 1, 1, 0, 0), (257, 128, 128, 1, 1, 0, 0),
+    (64, 512, 512, 64, 2, 0, 1), (200, 2176, 384, 8, 2, 0, 0), (7, 1920, 640, 16, 4, 128, 1),
     (9, 128, 16512, 2, 1, 0, 0), (70, 128, 16640, 2, 2, 128, 0), (70, 128, 4224, 4, 2, 0, 1), (70, 128, 1152, 4, 2, 128, 1)])
 def test_expert_ffn(T, H, I, E, K, cap, empty):
     wl = I8.INT8_SMALL.with_(T=T, H=H, I=I, E=E, K=K, masked_cap=cap)
