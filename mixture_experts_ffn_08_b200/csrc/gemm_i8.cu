@@ -3,8 +3,6 @@
 #include <cudaTypedefs.h>
 #include <math_constants.h>
 
-#include <atomic>
-
 #include "internal.h"
 #include "tc_gemm_i8.cuh"
 
@@ -56,19 +54,6 @@ bool make_tmap_out(CUtensorMap* m, void* ptr, uint64_t rows, uint64_t cols, uint
 }
 
 long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
-
-// Lets a kernel use `bytes` of dynamic shared memory, once per device (`done`: one bit each).
-template <class Kern>
-cudaError_t allow_smem(Kern kern, int bytes, std::atomic<unsigned long long>& done) {
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if ((done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return err;
-}
 
 // A [a_rows, K] (row stride lda), B [b_rows, K] (row stride ldb; b1: SWIGLU's up weights).
 template <class Cfg>
