@@ -121,10 +121,13 @@ def lib(require_gpu: bool = True):
     return _lib
 
 
+_Tensor = torch.Tensor
+
+
 def _ptr(t):
     if t is None:
         return None
-    if isinstance(t, torch.Tensor):
+    if type(t) is _Tensor or isinstance(t, _Tensor):
         return t.data_ptr()
     return int(t)
 

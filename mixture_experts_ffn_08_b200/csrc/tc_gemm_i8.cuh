@@ -12,8 +12,10 @@
 // 256 x BN tile with one stream of cta_group::2 MMAs, each CTA holding 128 rows of A and half
 // of the BN rows of B; the operand bytes that cross L2 -> SM per MAC are those of a 256 x 256
 // tile while each SM's TMEM still holds two accumulators, so the epilogue of one tile runs
-// under the main loop of the next.  (At K = 1536 a tile's MMAs last only 6000 cycles: an
-// epilogue that the main loop had to wait for would cost a third of that.)
+// under the main loop of the next.  (At K = 1536 a tile's MMAs last only 6000 cycles and its
+// epilogue nearly as long.)  Narrower one-SM tiles spread few rows over more SMs.
+// What bounds it on B200: the power cap for large products (8192 x 14336 x 4096 in 294-311 us, the
+// tensor pipe busy 96 % of the cycles at 1.6 GHz), HBM for a decode batch's weights (6.2 TB/s).
 // A group's first row is a multiple of 128, not of 256: the second half of a group's last pair
 // tile may lie past the group, and then it is neither loaded nor stored.
 //
@@ -903,7 +905,7 @@ MOE_DEVINL int4 ld_stream(const int4* p, bool in) {
 // One to four rows: nothing to share in a tile, the weights are read once whatever is done with
 // them.  A warp per R output channels, 16 codes per lane and load, integer dot products; the few
 // rows of A come from L1, each load of them used for R channels.  R * UNROLL loads of weights are
-// in flight per lane.
+// in flight per lane.  1 x 4096 x 7168 takes 6.5 us (4.5 TB/s), most of the rest the first bytes' way.
 template <int M, int R>
 __global__ void __launch_bounds__(256) i8_gemv_kernel(const int8_t* __restrict__ a, int64_t lda,
                                                       const int8_t* __restrict__ w, int64_t ldw, const I8Params p) {
