@@ -35,7 +35,7 @@ bool make_tmap_i8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Output [rows, cols] of 2- or 4-byte elements, row stride ld elements: boxes of 32 rows x 64
+// Output [rows, cols] of 2- or 4-byte elements, row stride ld elements: boxes of 32 rows x 128
 // bytes.  False where the rows do not start and end on 16-byte borders (the store unit clips a box
 // at such a border: it was seen to write past cols); the kernel then stores element by element.
 bool make_tmap_out(CUtensorMap* m, void* ptr, uint64_t rows, uint64_t cols, uint64_t ld, bool wide) {
@@ -46,10 +46,10 @@ bool make_tmap_out(CUtensorMap* m, void* ptr, uint64_t rows, uint64_t cols, uint
     return false;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {ld * esz};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / esz), 32};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esz), 32};
   cuuint32_t estr[2] = {1, 1};
   return fn(m, wide ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, ptr, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

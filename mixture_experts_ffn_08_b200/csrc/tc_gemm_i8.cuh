@@ -36,7 +36,7 @@
 namespace moe {
 
 constexpr int kI8MaxGroups = 1024;
-constexpr int kI8OutBox = 32 * 64;  // bytes of an output box: 32 rows x 64 bytes
+constexpr int kI8OutBox = 32 * 128;  // bytes of an output box: 32 rows x 128 bytes
 constexpr int kI8SmallRows = 32;  // an M-tile of at most this many rows loads this many of A
 
 struct I8Params {
@@ -96,14 +96,13 @@ struct I8Cfg {
   static constexpr int B_BYTES = B_ROWS * BK;
   static constexpr int BLOCK_BYTES = A_BYTES + B_BYTES;
   static constexpr int STAGE_BYTES = SUB * BLOCK_BYTES;
-  static constexpr int OUT_BYTES = 4 * 2 * kI8OutBox;  // two boxes per epilogue warp
+  static constexpr int OUT_BYTES = 4 * kI8OutBox;  // one box per epilogue warp
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + 1024;
   static constexpr int OUT_COLS = SWIGLU ? BN / 2 : BN;
   static constexpr int TMEM_COLS = 2 * BN;       // two accumulators
   static constexpr int TILE_M = 128 * CG;
   static constexpr int THREADS = 192;
-  static_assert(BN == 32 || BN == 64 || BN == 128 || BN == 256, "two accumulators in a power of two of TMEM columns");
-  static_assert(!SWIGLU || BN >= 64, "a SwiGLU tile is half gate and half up rows");
+  static_assert(BN == 64 || BN == 128 || BN == 256, "two accumulators in a power of two of TMEM columns");
   static_assert(CG == 1 || BN == 256, "pair tiles are 256 x 256");
   static_assert(SMEM_BYTES + 8 * (kI8MaxGroups + 1) + 4 * 512 * 4 + 512 <= 227 * 1024, "shared memory");
 };
@@ -226,24 +225,33 @@ MOE_DEVINL void i8_store1(const I8Params& p, long long row, int col, float v) {
   else static_cast<__half*>(p.out)[at] = __float2half_rn(v);
 }
 
-// ---- output boxes: 32 rows x 64 bytes, 64-byte swizzle (16-byte piece j of row r at
-// j ^ (r / 2 & 3)), two per warp.
+// ---- output boxes: 32 rows x 128 bytes, 128-byte swizzle (16-byte piece j of row r at
+// j ^ (r & 7)), one per warp.
 // Direct stores of a lane's own row touch 32 lines per instruction; measured on B200 they cost
 // the 8192 x 14336 x 4096 product 16 of 345 us and the 128-expert prefill 300 of 2690 us, where
-// the TMA unit writes whole segments on its own.
+// the TMA unit writes whole segments on its own.  (Two boxes of 64-byte rows: 16384 x 4096 x 1536 to
+// bf16 88 us against 80.)
 struct I8Boxes {
   uint8_t* base;
-  MOE_DEVINL void put(int i, int lane, const uint32_t* w) {
+  // A box that starts at (row, col): w0 and w1 are the halves of this lane's row.
+  MOE_DEVINL void store(const CUtensorMap* m, int lane, int row, int col, const uint32_t* w0, const uint32_t* w1) {
+    // (this warp's earlier store has read the box)
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint4*>(base + i * kI8OutBox + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-          make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-  }
-  MOE_DEVINL void send(const CUtensorMap* m, int i, int col, int row) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     reinterpret_cast<uint64_t>(m)),
-                 "r"(col), "r"(row), "r"(smem_u32(base + i * kI8OutBox))
-                 : "memory");
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t* w = j < 4 ? w0 + 4 * j : w1 + 4 * (j - 4);
+      *reinterpret_cast<uint4*>(base + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                       reinterpret_cast<uint64_t>(m)),
+                   "r"(col), "r"(row), "r"(smem_u32(base))
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
   }
   // 32 outputs of each of the warp's rows, the first `rows` of which are real, columns col .. col +
   // n - 1: through the boxes as 32 x 32 words (word c of row r at c ^ r), so that a warp stores along
@@ -278,27 +286,10 @@ struct I8Boxes {
         if (r < rows) *out = static_cast<T>(x[r]);
     }
   }
-  // Two boxes side by side, `width` columns each, that start at (row, col); w0, w1: 16 words of
-  // this lane's row.  The second one is left out where it starts past n_cols.
-  MOE_DEVINL void store2(const CUtensorMap* m, int lane, int row, int col, int width, int n_cols, const uint32_t* w0,
-                         const uint32_t* w1) {
-    // (this warp's earlier stores have read their boxes)
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    __syncwarp();
-    put(0, lane, w0);
-    put(1, lane, w1);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) {
-      send(m, 0, col, row);
-      if (col + width < n_cols) send(m, 1, col + width, row);
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    }
-  }
 };
 
 // tmA: boxes of 128 rows of A, tmA32: of 32.  tmB0 (and tmB1, the up weights of SWIGLU): boxes
-// of B_ROWS rows, or of BN / 2 for SWIGLU.  tmOut (with p.tma_store): boxes of 32 rows x 64 bytes.
+// of B_ROWS rows, or of BN / 2 for SWIGLU.  tmOut (with p.tma_store): boxes of 32 rows x 128 bytes.
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tc_gemm_i8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
@@ -496,7 +487,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;  // TMEM lane quadrant
     float* cols = col_sh[q];
-    I8Boxes out_boxes{smem + STAGES * Cfg::STAGE_BYTES + q * 2 * kI8OutBox};
+    I8Boxes out_boxes{smem + STAGES * Cfg::STAGE_BYTES + q * kI8OutBox};
     // a row's 32 outputs are whole 32-byte sectors
     const bool whole = ((reinterpret_cast<uintptr_t>(p.out) |
                          static_cast<uintptr_t>(p.ldo * (Cfg::SWIGLU || p.out_type == MOE_OUT_FP32 ? 4 : 2))) & 31) == 0;
@@ -543,43 +534,42 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) rg[i] = __float_as_uint(silu_mul(g[i], u[i]));
           if (boxes) {
-            out_boxes.store2(&tmOut, lane, box_row, col0 + c, 16, p.N, rg, rg + 16);
+            out_boxes.store(&tmOut, lane, box_row, col0 + c, rg, rg + 16);
           } else if (row_ok) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) st_global_v8(out + c + 8 * i, rg + 8 * i);
           }
         }
       } else {
-        // 64 columns at a time (32 in the narrowest tile): one wait and one fence for two boxes
-        constexpr int H = BN >= 64 ? 2 : 1;
+        // 64 columns at a time: one wait and one fence for a box of 16-bit outputs
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 32 * H) {
-          uint32_t r[H][32];
+        for (int c = 0; c < BN; c += 64) {
+          uint32_t r[2][32];
 #pragma unroll
-          for (int j = 0; j < H; ++j) tmem_ld_32x32b_x32(tbase + c + 32 * j, r[j]);
+          for (int j = 0; j < 2; ++j) tmem_ld_32x32b_x32(tbase + c + 32 * j, r[j]);
           tmem_ld_wait(r[0]);
-          if constexpr (H == 2) reg_fence(r[1]);
+          reg_fence(r[1]);
           if (col0 + c >= p.N) continue;
           if (boxes && p.out_type != MOE_OUT_FP32) {
             uint32_t w[2][16];
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
+            for (int j = 0; j < 2; ++j) {
               float v[32];
               i8_scale32(r[j], sa, cols + c + 32 * j, p.bias != nullptr ? cols + 256 + c + 32 * j : nullptr, v);
               i8_pack32(p.out_type, v, w[j]);
             }
-            out_boxes.store2(&tmOut, lane, box_row, col0 + c, 32, H == 2 ? p.N : 0, w[0], w[H - 1]);
+            out_boxes.store(&tmOut, lane, box_row, col0 + c, w[0], w[1]);
           } else {
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
+            for (int j = 0; j < 2; ++j) {
               const int col = col0 + c + 32 * j;
               if (col >= p.N) continue;
               float v[32];
               i8_scale32(r[j], sa, cols + c + 32 * j, p.bias != nullptr ? cols + 256 + c + 32 * j : nullptr, v);
-              if (boxes)
-                out_boxes.store2(&tmOut, lane, box_row, col, 16, p.N, reinterpret_cast<const uint32_t*>(v),
-                                 reinterpret_cast<const uint32_t*>(v) + 16);
-              else if (whole && p.N - col >= 32) {
+              if (boxes) {
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+                out_boxes.store(&tmOut, lane, box_row, col, w, w + 16);
+              } else if (whole && p.N - col >= 32) {
                 if (row_ok) i8_store32(p, row, col, v, 32);
               } else if (rows_here > 0) {
                 out_boxes.store_rows(p, lane, row - lane, rows_here, col, v, p.N - col);
