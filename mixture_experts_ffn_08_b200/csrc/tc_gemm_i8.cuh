@@ -230,7 +230,7 @@ MOE_DEVINL void i8_store1(const I8Params& p, long long row, int col, float v) {
 // Direct stores of a lane's own row touch 32 lines per instruction; measured on B200 they cost
 // the 8192 x 14336 x 4096 product 16 of 345 us and the 128-expert prefill 300 of 2690 us, where
 // the TMA unit writes whole segments on its own.  (Two boxes of 64-byte rows: 16384 x 4096 x 1536 to
-// bf16 88 us against 80.)
+// bf16 91 us against 87, medians of five.)
 struct I8Boxes {
   uint8_t* base;
   // A box that starts at (row, col): w0 and w1 are the halves of this lane's row.

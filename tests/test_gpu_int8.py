@@ -350,6 +350,44 @@ def test_expert_ffn_streams_and_graphs():
         check()
 
 
+FIRST = """
+import torch
+from mixture_experts_ffn_08_b200 import binding as B, workloads as W
+for M, N, K in ((1, 512, 512), (8, 512, 4096), (128, 2048, 1024), (500, 4096, 256), (4096, 4096, 128), (16, 20000, 128)):
+    a = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda")
+    w = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda")
+    one_a, one_w, out = torch.ones(M, device="cuda"), torch.ones(N, device="cuda"), torch.zeros((M, N), device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.check(B.moe_linear_int8(M, N, K, a, K, one_a, w, K, one_w, None, out, N, B.MOE_OUT_FP32, None))
+    g.replay()
+    assert torch.equal(out.double(), a.double() @ w.double().T), (M, N, K)
+for T, H, dtype in ((1, 7168, W.DTYPE_BF16), (300, 1024, W.DTYPE_BF16), (20, 20480, W.DTYPE_BF16)):
+    p = B.params(W.Workload("first", T=T, H=H, I=128, E=2, K=1, dtype=dtype))
+    x = torch.randn((T, H), device="cuda").bfloat16()
+    w, out, again = torch.ones(H, device="cuda").bfloat16(), torch.zeros_like(x), torch.zeros_like(x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.check(B.moe_add_rms_norm(p, x, None, w, 1e-6, None, out, None))
+    g.replay()
+    B.check(B.moe_add_rms_norm(p, x, None, w, 1e-6, None, again, None))
+    assert torch.equal(out, again) and out.float().abs().sum() > 0
+print("captured")
+"""
+
+
+def test_first_call_inside_a_capture():
+    """A process whose first call of each kernel is captured: its one-time settings need no stream."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
 # -------------------------------------------------------------------------------------- layer
 LAYERS = [dict(), dict(T=1), dict(T=5, E=300, K=8, n_group=4, topk_group=2, group_topn=2, score_fn=W.SCORE_SIGMOID, has_bias=True),
           dict(T=300, E=4, masked_cap=384), dict(T=700, E=4, H=512, I=384), dict(T=1100, E=4), dict(T=40, skewed=True, E=16)]
