@@ -493,23 +493,43 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                          static_cast<uintptr_t>(p.ldo * (Cfg::SWIGLU || p.out_type == MOE_OUT_FP32 ? 4 : 2))) & 31) == 0;
     const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&tempty_bar[0]), 0) : 0u;
     const uint32_t tempty1 = PAIR ? mapa_shared(smem_u32(&tempty_bar[1]), 0) : 0u;
+    // A tile's scales are on their way while the tile before it is stored (read at its start they cost
+    // 142 experts of 384 x 2048 with five rows each 121 us for 88, 81 of 896 x 384 with 477 126 for 111).
+    constexpr int PER = Cfg::OUT_COLS / 32;
+    I8Tile next;
+    float next_sa = 0.f, next_cols[PER], next_more[PER];
+    auto fetch = [&](int item) {
+      next = i8_decode<Cfg>(item, NT, p, pref, cnt);
+      const int col0 = next.n_tile * Cfg::OUT_COLS;
+      const long long wrow = static_cast<long long>(next.group) * p.N + col0;
+      const int in_tile = 128 * static_cast<int>(rank) + q * 32 + lane;
+      next_sa = next.m0 + in_tile < next.count ? __ldg(p.a_scale + next.row0 + in_tile) : 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int c = 32 * i + lane;
+        const bool in = col0 + c < p.N;
+        next_cols[i] = in ? __ldg(p.w_scale + wrow + c) : 0.f;
+        if constexpr (Cfg::SWIGLU) next_more[i] = in ? __ldg(p.w_scale_up + wrow + c) : 0.f;
+        else next_more[i] = in && p.bias != nullptr ? __ldg(p.bias + col0 + c) : 0.f;
+      }
+    };
+    if (first_item < total) fetch(first_item);
     int acc = 0;
     uint32_t acc_ph = 0;
     for (int item = first_item; item < total; item += step) {
-      const I8Tile t = i8_decode<Cfg>(item, NT, p, pref, cnt);
+      const I8Tile t = next;
       const int col0 = t.n_tile * Cfg::OUT_COLS;
-      const long long wrow = static_cast<long long>(t.group) * p.N + col0;
       const int in_tile = 128 * static_cast<int>(rank) + q * 32 + lane;
       const long long row = t.row0 + in_tile;
       const bool row_ok = t.m0 + in_tile < t.count;
-      const float sa = row_ok ? __ldg(p.a_scale + row) : 0.f;
+      const float sa = next_sa;
       __syncwarp();
-      for (int c = lane; c < Cfg::OUT_COLS; c += 32) {
-        const bool in = col0 + c < p.N;
-        cols[c] = in ? __ldg(p.w_scale + wrow + c) : 0.f;
-        if constexpr (Cfg::SWIGLU) cols[128 + c] = in ? __ldg(p.w_scale_up + wrow + c) : 0.f;
-        else cols[256 + c] = in && p.bias != nullptr ? __ldg(p.bias + col0 + c) : 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        cols[32 * i + lane] = next_cols[i];
+        cols[(Cfg::SWIGLU ? 128 : 256) + 32 * i + lane] = next_more[i];
       }
+      if (item + step < total) fetch(item + step);
       __syncwarp();
       const bool ready = __all_sync(0xffffffffu, mbar_wait_bounded(&tfull_bar[acc], acc_ph, &abort_flag));
       if (!ready) break;
