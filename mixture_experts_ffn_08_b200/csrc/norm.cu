@@ -50,6 +50,7 @@ struct NormParams {
 
 // (|v| as an integer keeps the order of the values, infinities above them and NaN above those)
 constexpr uint32_t kInfBits = 0x7f800000u;
+constexpr uint32_t kSmallBits = 0x05000000u;  // 2^-117: 448 / m of what lies below may be infinite
 
 // Biased exponent (e + 127, at least 1) of the smallest 2^e with v <= 448 * 2^e, for the value
 // v = m * rstd > 0 (448 = 1.75 * 2^8: a significand above 1.75 carries into the exponent).
@@ -174,17 +175,29 @@ MOE_DEVINL void store_vec(const float2 (&zw)[4], float m, const RowScale& r, con
   } else if constexpr (FMT == NORM_E4M3) {
     float2 y[4];
     float s = 1.f;
-    if (r.bad || __float_as_uint(m) >= kInfBits) {
-      s = CUDART_NAN_F;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = make_float2(0.f, 0.f);
-    } else {
-      const int e = m > 0.f ? e4m3_scale_bits(m, r.factor, r.rstd) : 127;
+    const uint32_t mb = __float_as_uint(m);
+    if (!r.bad && mb - kSmallBits < kInfBits - kSmallBits) {
+      const int e = e4m3_scale_bits(m, r.factor, r.rstd);
       s = __int_as_float(e << 23);
       const float inv = __int_as_float((254 - e) << 23);
       const float2 f = make_float2(r.factor * inv, r.factor * inv), g = make_float2(r.rest * inv, r.rest * inv);
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[i] = fma2(zw[i], f, mul2(zw[i], g));
+    } else if (r.bad || mb >= kInfBits) {
+      s = CUDART_NAN_F;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = make_float2(0.f, 0.f);
+    } else {
+      // rstd / s, which is about 448 / m, may pass fp32's range: z w is divided by s first
+      const int e = m > 0.f ? e4m3_scale_bits(m, r.factor, r.rstd) : 127;
+      s = __int_as_float(e << 23);
+      const float inv = __int_as_float((254 - e) << 23);
+      const float2 v = make_float2(inv, inv), f = make_float2(r.factor, r.factor), g = make_float2(r.rest, r.rest);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = mul2(zw[i], v);
+        y[i] = fma2(t, f, mul2(t, g));
+      }
     }
     const float* yv = reinterpret_cast<const float*>(y);
     if (in) {
