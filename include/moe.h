@@ -274,8 +274,9 @@ moe_status_t moe_shared_expert_ffn(const moe_params_t* p, const void* x, const v
 /*   a [M,K] int8, rows lda bytes apart; a_scale [M] fp32 (as moe_add_rms_norm writes);   */
 /*   w [N,K] int8 (nn.Linear), rows ldw bytes apart; w_scale [N] fp32; bias [N] fp32 or   */
 /*   NULL; out [M,N] of out_type (moe_out_type_t), rows ldo elements apart; columns past  */
-/*   N are not touched.  The sum is exact; one rounding to out_type (fp16: to infinity    */
-/*   past 65504).                                                                        */
+/*   N are not touched.  The sum is exact; (sum * a_scale) * w_scale + bias in fp32 and  */
+/*   one rounding to out_type (fp16: to infinity past 65504).  A row's bits do not        */
+/*   depend on M.                                                                        */
 /* M 0..2^30, N 1..2^30; K a multiple of 16, 16..131056; lda and ldw multiples of 16; a    */
 /* and w 16-byte aligned; out overlaps no input.  No workspace.  device_status: optional device int32 that */
 /* the caller has zeroed; MOE_DEV_TIMEOUT is OR-ed into it.                               */

@@ -973,8 +973,9 @@ __global__ void __launch_bounds__(256) i8_gemv_kernel(const int8_t* __restrict__
       if (lane == r * M + m) mine = __int2float_rn(t);
     }
   const int n = n0 + lane / M, m = lane % M;
+  // (sum, row scale, channel scale, as everywhere: the product of the scales alone may leave fp32's range)
   if (lane < R * M && n < p.N)
-    i8_store1(p, m, n, fmaf(mine, __ldg(p.a_scale + m) * __ldg(p.w_scale + n), p.bias != nullptr ? __ldg(p.bias + n) : 0.f));
+    i8_store1(p, m, n, fmaf(mine * __ldg(p.a_scale + m), __ldg(p.w_scale + n), p.bias != nullptr ? __ldg(p.bias + n) : 0.f));
 }
 
 }  // namespace moe
