@@ -156,14 +156,17 @@ int64_t moe_max_padded_rows(const moe_params_t* p);
 /*   y   = z / sqrt(mean_h(z^2) + eps) * norm_w                                          */
 /*   out = y by p->dtype: bf16 [T,H] (out_scale unused); e4m3 codes with out_scale       */
 /*         [T,H/128] = 2^ceil(log2(amax/448)) of the 128 channels; int8 codes with         */
-/*         out_scale [T] = amax/127 of the token, code = y / scale to the nearest, ties to  */
-/*         even (scale 1 where amax = 0, and never below 2^-126)                           */
+/*         out_scale [T] = amax/127 of the token, code = 127 y / amax to the nearest, ties  */
+/*         to even (both scales: 1 where amax = 0, and never below 2^-126, where an int8    */
+/*         code is y / 2^-126 to the nearest)                                              */
 /*   x, residual, residual_out [T,H], norm_w [H] bf16; eps a positive normal number      */
 /* z is written to residual_out unless that is NULL; it may be residual itself, or x.    */
 /* Out may be x for the bf16 format without a residual.  Buffers that overlap otherwise  */
-/* are not supported.  Statistics in fp32 and fp64, one rounding.  In the 8-bit formats a */
-/* token with a NaN, an infinity or squares whose sum passes fp32's range gets codes 0   */
-/* and scale NaN.  Only p's T, H and dtype matter (the others must be valid).            */
+/* are not supported.  Statistics in fp32 and fp64, products z * norm_w in fp32.  In the  */
+/* 8-bit formats a token with a NaN, an infinity or squares whose sum passes fp32's range */
+/* gets codes 0 and scale NaN (bf16: what an infinite sum leaves, zeros or NaN), and so   */
+/* does one whose z * norm_w is no fp32 number (e4m3: the 128 channels around it).        */
+/* Only p's T, H and dtype matter (the others must be valid).                            */
 /* ---------------------------------------------------------------------------------- */
 moe_status_t moe_add_rms_norm(const moe_params_t* p, const void* x, const void* residual,
                               const void* norm_w, float eps, void* residual_out, void* out,

@@ -88,3 +88,36 @@ def test_e4m3_layer_of_a_token_with_one_smallest_number():
     B.check(B.moe_norm_layer_forward(p, x, None, w, EPS, None, *I8.layer_args(d)[2:], out, None, None, None, ws, ws.numel()))
     torch.cuda.synchronize()
     assert torch.isfinite(out).all() and B.moe_get_device_status(ws) == 0
+
+
+def int8_codes(x, w):
+    """Codes of the norm, and those of 127 z w / max |z w| in fp64: z w and its multiples are exact, and a
+    quotient that is not a tie lies more than 2^-30 from one, so rounding it decides as the exact one would."""
+    T, H = x.shape
+    out = torch.full((T, H), 77, dtype=torch.int8, device="cuda")
+    scale = torch.empty(T, device="cuda")
+    B.check(B.moe_add_rms_norm(params(T, H, W.DTYPE_INT8), x, None, w, EPS, None, out, scale))
+    zw = P.f64(x) * P.f64(w)[None, :]
+    return P.f64(out), np.round(127.0 * zw / np.abs(zw).max(axis=1, keepdims=True))
+
+
+@pytest.mark.parametrize("T,H", [(3, 256), (200, 256), (3, 8320), (2, 20608), (2, 26752)])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -112])
+def test_int8_ties_go_to_even(T, H, size):
+    """Every (2 k + 1) / 2 as the value of a code, for a largest product whose inverse rounds up or down."""
+    odd = torch.arange(1, 254, 2, dtype=torch.float32)
+    row = torch.cat([odd, -odd, torch.tensor([254.0, 0.0])]).repeat((H + 255) // 256)[:H]
+    x = (row * size).cuda().bfloat16().repeat(T, 1)
+    for q in range(1, 256, 2 if H == 256 else 46):
+        got, want = int8_codes(x, torch.full((H,), float(q), device="cuda").bfloat16())
+        np.testing.assert_array_equal(got, want)
+
+
+@pytest.mark.parametrize("T,H", [(2000, 1024), (100, 7168), (300, 8320), (200, 20608), (100, 26752)])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -112])
+def test_int8_codes_are_the_nearest(T, H, size):
+    g = I8.gen(T)
+    x = (torch.randn((T, H), generator=g, device="cuda") * size).bfloat16()
+    w = (1 + 0.2 * torch.randn(H, generator=g, device="cuda")).bfloat16()
+    got, want = int8_codes(exact_products(x, w), w)
+    np.testing.assert_array_equal(got, want)
