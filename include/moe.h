@@ -178,7 +178,8 @@ moe_status_t moe_add_rms_norm(const moe_params_t* p, const void* x, const void* 
 /*   x        [T,H] bf16, e4m3 codes with x_scale [T,H/128] (FP8), or int8 codes with   */
 /*            x_scale [T] (INT8: the codes enter the product, the scale the logits)     */
 /*   w_r      [E,H] bf16;  bias [E] fp32 or NULL                                        */
-/*   topk_ids [T,K] int32 out: experts in descending selection score (ties: lower id)   */
+/*   topk_ids [T,K] int32 out: experts in descending selection score (ties: lower id;   */
+/*            NaN scores last, so a token of NaN gets K different experts, weights NaN) */
 /*   topk_w   [T,K] fp32 out: weights from the unbiased scores                          */
 /* Uses ws for the logits (and, for FP8 and INT8, a bf16 copy of x).                   */
 /* ---------------------------------------------------------------------------------- */

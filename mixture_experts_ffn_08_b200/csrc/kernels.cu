@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(128) topk_kernel(
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = j * 32 + lane;
-    c[j] = e < E ? s[j] + (bias ? __ldg(bias + e) : 0.f) : -CUDART_INF_F;
+    // (a NaN, which no comparison orders, ranks last: the ids stay below E and differ)
+    c[j] = e < E ? fmaxf(s[j] + (bias ? __ldg(bias + e) : 0.f), -CUDART_INF_F) : -CUDART_INF_F;
   }
 
   if (n_group > 1) {
