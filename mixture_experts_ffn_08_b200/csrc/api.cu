@@ -8,6 +8,7 @@
 #include <vector>
 
 #include "../../include/moe.h"
+#include "i8_choice.h"
 #include "internal.h"
 
 namespace moe {
@@ -409,24 +410,13 @@ moe_status_t do_expert_ffn_i8(const moe_params_t* p, const void* x_perm, const f
   const Layout L = layout(p);
   int32_t* status = at<int32_t>(ws, L.status);
   float* h = at<float>(ws, L.h);
-  // Two-SM tiles where the average expert has 160 rows or more and the tiles go round the SM pairs
-  // twice, else one-SM tiles.  Measured on B200, 32 experts of 4096 x 1536: 192 rows each 159 us
-  // against 177, 128 rows 149 against 138; eight experts of 1024 x 512, 512 rows each (16 x 4 pair
-  // tiles) 34 against 26.  (The kernels take the schedule from the counts, in both layouts.)
-  const long long P = static_cast<long long>(p->T) * p->K;
-  const bool tall = P >= 160LL * p->E;
-  const long long m_tiles = P / kBlockM + (P < p->E ? P : p->E);  // at most
-  const int rows = static_cast<int>(P / p->E < kBlockM ? P / p->E : kBlockM);
-  const bool pair_gu = tall && P / 256 * (p->I / 128) >= num_sms();
-  const bool pair_dn = tall && P / 256 * ((p->H + 255) / 256) >= num_sms();
-  const int tile_gu = pair_gu ? kI8PairTile : i8_tile_width(m_tiles, rows, 2LL * p->I);
-  const int tile_dn = pair_dn ? kI8PairTile : i8_tile_width(m_tiles, rows, p->H);
+  const I8ExpertTiles tiles = i8_expert_tiles(static_cast<long long>(p->T) * p->K, p->E, p->H, p->I, num_sms());
   const I8Rows x{x_perm, x_perm_scale, L.max_rows, offsets, counts, p->E, p->masked_cap};
   const I8Rows hq{at<void>(ws, L.hq), at<float>(ws, L.hq_scale), L.max_rows, offsets, counts, p->E, p->masked_cap};
-  MOE_CUDA(gemm_i8_gateup_swiglu(x, w_gate, w_up, gate_scale, up_scale, p->I, p->H, h, status, tile_gu, st));
+  MOE_CUDA(gemm_i8_gateup_swiglu(x, w_gate, w_up, gate_scale, up_scale, p->I, p->H, h, status, tiles.gate_up, st));
   MOE_CUDA(launch_quant_rows(h, L.max_rows, offsets, counts, p->E, p->masked_cap, p->I, at<void>(ws, L.hq),
                              at<float>(ws, L.hq_scale), st));
-  MOE_CUDA(gemm_i8_down(hq, w_down, down_scale, p->H, p->I, y_perm, status, tile_dn, st));
+  MOE_CUDA(gemm_i8_down(hq, w_down, down_scale, p->H, p->I, y_perm, status, tiles.down, st));
   return MOE_OK;
 }
 

@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 #include <math_constants.h>
 
+#include "i8_choice.h"
 #include "internal.h"
 #include "tc_gemm_i8.cuh"
 
@@ -53,7 +54,7 @@ bool make_tmap_out(CUtensorMap* m, void* ptr, uint64_t rows, uint64_t cols, uint
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+long long cdiv(long long a, long long b) { return i8_cdiv(a, b); }
 
 // A [a_rows, K] (row stride lda), B [b_rows, K] (row stride ldb; b1: SWIGLU's up weights).
 template <class Cfg>
@@ -378,25 +379,6 @@ cudaError_t launch_quant_rows(const float* h, long long max_rows, const int32_t*
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-// Rounds of tiles times the ns that a K-block of one takes (as in gemm_i8_linear).  One token through
-// two of eight experts of 4096 x 14336: 75 us, 94 with tiles of 256 alone; 33 tokens through eight of
-// 256 x 128: 10.5 us against 13.6.  A batch that fills the SMs many times keeps the widest tiles, which
-// read the rows of A least often.
-int i8_tile_width(long long m_tiles, int tile_rows, long long rows) {
-  const long long sms = num_sms();
-  int best_bn = 256;
-  float best = -1.f;
-  for (int bn = 256; bn >= 64; bn /= 2) {
-    const float r = (tile_rows <= kI8SmallRows ? kI8SmallRows : 128) + bn, issue = 140.f + r * 0.2f, load = r * 0.94f;
-    const float cost = cdiv(m_tiles * cdiv(rows, bn), sms) * (issue > load ? issue : load);
-    if (best < 0.f || cost < best) {
-      best = cost;
-      best_bn = bn;
-    }
-  }
-  return best_bn;
-}
-
 cudaError_t gemm_i8_gateup_swiglu(const I8Rows& a, const void* w_gate, const void* w_up, const float* gate_scale,
                                   const float* up_scale, int N, int K, float* h, int32_t* status, int tile,
                                   cudaStream_t st) {
@@ -465,52 +447,23 @@ cudaError_t gemm_i8_linear(int M, int N, int K, const void* a, int64_t lda, cons
   p.out_type = out_type;
   p.ldo = ldo;
   p.status = status;
-  const long long sms = num_sms();
-  // One to four rows: dot products, which read each row of A once per channel, where that beats the
-  // tensor cores (us, dot products and tensor cores: 2 x 4096 x 7168 7.4 and 8.6, 2 x 256 x 14336 8.5
-  // and 7.2, 3 x 6144 x 4096 6.8 and 8.3, 3 x 576 x 7168 7.6 and 5.2, 4 x 512 x 4096 3.0 and 3.8,
-  // 4 x 6144 x 4096 9.5 and 8.2).  Two channels per warp for two rows of three blocks per SM or
-  // more: 2 x 7168 x 2048 3.9 against 4.6, 2 x 5120 x 2048 3.3 against 3.1.
-  if (M == 1) return launch_i8_gemv<1, 1>(a, lda, w, ldw, p, st);
-  if (M == 2 && K <= 8192 && N >= 48 * sms) return launch_i8_gemv<2, 2>(a, lda, w, ldw, p, st);
-  if (M == 2 && K <= 8192) return launch_i8_gemv<2, 1>(a, lda, w, ldw, p, st);
-  const bool few_macs = K <= 4096 && static_cast<long long>(N) * K * (M - 1) <= (48LL << 20);
-  if (M == 3 && few_macs) return launch_i8_gemv<3, 1>(a, lda, w, ldw, p, st);
-  if (M == 4 && few_macs) return launch_i8_gemv<4, 1>(a, lda, w, ldw, p, st);
-  const long long mt = cdiv(M, 128), pairs = cdiv(M, 256) * cdiv(N, 256);
-  // More 128 x 128 tiles than SMs: persistent, two-SM tiles for more than 128 rows (where those tiles
-  // fit one round the other kernel is faster: 512 x 4736 x 4096 11.7 us against 16.2, 256 x 9472 x 1024
-  // 6.6 against 9.7)
-  if (mt * cdiv(N, 128) > sms) {
-    if (M > 128) return launch_i8<I8Cfg<2, 256, false, 6>>(a, M, lda, w, w, N, ldw, p, pairs, MOE_K_LINEAR, st);
-    if (cdiv(cdiv(N, 256), sms) * 2 <= cdiv(cdiv(N, 128), sms))
-      return launch_i8<I8Cfg<1, 256, false, 4>>(a, M, lda, w, w, N, ldw, p, cdiv(N, 256), MOE_K_LINEAR, st);
+  const I8Choice c = i8_linear_choice(M, N, K, num_sms());
+  if (c.kernel == I8_DOT) {
+    if (M == 1) return launch_i8_gemv<1, 1>(a, lda, w, ldw, p, st);
+    if (M == 2 && c.channels == 2) return launch_i8_gemv<2, 2>(a, lda, w, ldw, p, st);
+    if (M == 2) return launch_i8_gemv<2, 1>(a, lda, w, ldw, p, st);
+    if (M == 3) return launch_i8_gemv<3, 1>(a, lda, w, ldw, p, st);
+    return launch_i8_gemv<4, 1>(a, lda, w, ldw, p, st);
+  }
+  if (c.kernel == I8_PERSISTENT) {
+    if (c.bn == kI8PairTile)
+      return launch_i8<I8Cfg<2, 256, false, 6>>(a, M, lda, w, w, N, ldw, p, cdiv(M, 256) * cdiv(N, 256), MOE_K_LINEAR, st);
+    if (c.bn == 256) return launch_i8<I8Cfg<1, 256, false, 4>>(a, M, lda, w, w, N, ldw, p, cdiv(N, 256), MOE_K_LINEAR, st);
     return launch_i8<I8Cfg<1, 128, false, 3, 2>>(a, M, lda, w, w, N, ldw, p, cdiv(N, 128), MOE_K_LINEAR, st);
   }
-  // One round of tiles of 128 x bn over ks parts of K each: the shortest by this estimate in ns,
-  // fitted to 170 shapes of 8 to 512 rows (0.6 % above the best choice, 8 % at most).  A K-block
-  // takes its issue or its bytes, and the longer the more CTAs load; a tile its sums; parts an
-  // exchange.  Clusters of four do not reach all SMs (144 CTAs of them took two rounds).
-  const int KB = static_cast<int>(cdiv(K, 128)), box = M <= 32 ? 32 : (M <= 64 ? 64 : 128);
-  int best_bn = 128, best_ks = 1;
-  float best = -1.f;
-  for (int bn = 32; bn <= 128; bn *= 2)
-    for (int ks = 1; ks <= 4 && ks * 2 <= KB + 1; ks *= 2) {
-      const long long ctas = mt * cdiv(N, bn) * ks;
-      if (ctas > (ks == 4 ? sms - 20 : sms)) continue;
-      const float rows = box + bn, sums = bn * box;
-      const float issue = 140.f + rows * 0.2f, load = rows * 0.94f;
-      const float cost = cdiv(KB, ks) * ((issue > load ? issue : load) + ctas * rows * 0.001f) + sums / 15.f +
-                         (ks > 1 ? 200.f + sums * 0.19f : 0.f);
-      if (best < 0.f || cost < best) {
-        best = cost;
-        best_bn = bn;
-        best_ks = ks;
-      }
-    }
-  if (M <= 32) return launch_i8_split_rows<32>(a, lda, w, ldw, p, best_bn, best_ks, st);
-  if (M <= 64) return launch_i8_split_rows<64>(a, lda, w, ldw, p, best_bn, best_ks, st);
-  return launch_i8_split_rows<128>(a, lda, w, ldw, p, best_bn, best_ks, st);
+  if (c.rows == 32) return launch_i8_split_rows<32>(a, lda, w, ldw, p, c.bn, c.ks, st);
+  if (c.rows == 64) return launch_i8_split_rows<64>(a, lda, w, ldw, p, c.bn, c.ks, st);
+  return launch_i8_split_rows<128>(a, lda, w, ldw, p, c.bn, c.ks, st);
 }
 
 }  // namespace moe

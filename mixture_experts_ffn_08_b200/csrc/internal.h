@@ -210,11 +210,7 @@ struct I8Rows {
   int G;
   int masked_cap;
 };
-// h [rows, N] fp32 = SiLU(A Wg^T) * (A Wu^T) on the real rows.  pair: tiles of two CTAs.
-// Width of a one-SM tile for m_tiles tiles of about tile_rows rows by `rows` weight rows (both of gate
-// and up): the narrower ones where the wide ones leave SMs idle.
-int i8_tile_width(long long m_tiles, int tile_rows, long long rows);
-constexpr int kI8PairTile = 0;  // `tile` below: 256 x 256 over two SMs, else a width
+// h [rows, N] fp32 = SiLU(A Wg^T) * (A Wu^T) on the real rows.  tile: as i8_choice.h names it.
 cudaError_t gemm_i8_gateup_swiglu(const I8Rows& a, const void* w_gate, const void* w_up, const float* gate_scale,
                                   const float* up_scale, int N, int K, float* h, int32_t* status, int tile,
                                   cudaStream_t st);

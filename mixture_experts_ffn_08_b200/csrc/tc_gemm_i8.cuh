@@ -31,13 +31,13 @@
 
 #include <type_traits>
 
+#include "i8_choice.h"
 #include "tc_gemm_2cta.cuh"
 
 namespace moe {
 
 constexpr int kI8MaxGroups = 1024;
 constexpr int kI8OutBox = 32 * 128;  // bytes of an output box: 32 rows x 128 bytes
-constexpr int kI8SmallRows = 32;  // an M-tile of at most this many rows loads this many of A
 
 struct I8Params {
   const int32_t* offsets;  // [G+1] first row of each group (contiguous layout, grouped)

@@ -8,6 +8,7 @@ from mixture_experts_ffn_08_b200 import binding as B
 from mixture_experts_ffn_08_b200 import inputs
 from tests import int8_help as I8
 from tests import parity as P
+from tests import test_gpu_int8 as G
 
 pytestmark = pytest.mark.gpu
 
@@ -36,6 +37,18 @@ def test_linear_pair_tiles_at_every_row_count():
         out = torch.empty((M, N), device="cuda")
         B.check(B.moe_linear_int8(M, N, K, a, K, one_a, w, K, one_w, None, out, N, B.MOE_OUT_FP32, None))
         assert torch.equal(out, ref[:M]), M
+
+
+# Two rows and so many channels that a warp takes two of them; the last warp has one where N is odd.
+TWO_CHANNELS = [(2, 7104, 16), (2, 7105, 528), (2, 7333, 1040), (2, 9999, 8192), (2, 20001, 4112)]
+
+
+@pytest.mark.parametrize("M,N,K", TWO_CHANNELS)
+def test_linear_of_two_rows_and_two_channels(M, N, K):
+    for i, dtype in enumerate(G.KIND):
+        args, ref, tol = G.linear_case(M, N, K, dtype, bias=i == 1, pad=(16, 32, (0, 1, 8)[i]), seed=N + i)
+        G.linear(*args)
+        G.check_linear(args, ref, tol)
 
 
 @pytest.mark.parametrize("more", [0, 256])
