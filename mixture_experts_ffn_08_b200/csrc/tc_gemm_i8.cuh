@@ -54,7 +54,7 @@ struct I8Params {
   void* out;               // SWIGLU: fp32 [rows, ldo]; else out_type
   int out_type;            // moe_out_type_t
   int tma_store;           // the output's tensor map is usable (16-byte aligned rows)
-  int prefetch;            // few rows: all blocks are resident at once
+  int prefetch;            // dot products: ask for the first weights before waiting for the kernel before
   int64_t ldo;
   int32_t* status;
 };
@@ -899,7 +899,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   }
 }
 
-// 16 bytes read once (zero where !in); volatile, so that a batch of them is issued as a batch.
+// 16 bytes read once (zero where !in); volatile: issued in the order written.
 MOE_DEVINL int4 ld_stream(const int4* p, bool in) {
   int4 v;
   asm volatile(
@@ -914,8 +914,9 @@ MOE_DEVINL int4 ld_stream(const int4* p, bool in) {
 
 // One to four rows: nothing to share in a tile, the weights are read once whatever is done with
 // them.  A warp per R output channels, 16 codes per lane and load, integer dot products; the few
-// rows of A come from L1, each load of them used for R channels.  R * UNROLL loads of weights are
-// in flight per lane.  1 x 4096 x 7168 takes 6.5 us (4.5 TB/s), most of the rest the first bytes' way.
+// rows of A come from L1, each load of them used for R channels.  Many warps keep the loads in
+// flight, 64 an SM for one row (32 registers), 32 for four (52).  1 x 4096 x 7168 takes 6.5 us (4.5
+// TB/s), most of the rest the first bytes' way.
 template <int M, int R>
 __global__ void __launch_bounds__(256) i8_gemv_kernel(const int8_t* __restrict__ a, int64_t lda,
                                                       const int8_t* __restrict__ w, int64_t ldw, const I8Params p) {
@@ -924,8 +925,8 @@ __global__ void __launch_bounds__(256) i8_gemv_kernel(const int8_t* __restrict__
   const int lane = lane_id();
   const int n0 = (blockIdx.x * 8 + warp_id()) * R;
   // The first 4 KB of the warp's weights on their way into L2 while the kernel before this one still
-  // runs, where all blocks are resident at once.  A prefetch is not a read: whatever that kernel
-  // writes there is what is loaded below.
+  // runs: for the blocks that start before it ends.  (One that starts later asks just before it loads.)
+  // A prefetch is not a read: whatever that kernel writes there is what is loaded below.
   if (p.prefetch) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
