@@ -15,7 +15,7 @@
 // 1e-7 of a border and not within 1e-6.  An int8 code is taken from two estimates of 127 / max|z w|, next
 // below and above it; where they disagree, z w and the border between the codes are compared exactly,
 // and a tie goes to the even code.  (One estimate alone put 166 of 8 million codes, and half of the
-// ties, on the wrong side.  The second costs 1 % of 16384 x 7168 with a residual, 8 % without, 0.1 of
+// ties, on the wrong side.  The second costs 1 % of 16384 x 7168 with a residual, 6 % without, 0.15 of
 // 3.4 us for 128 rows.)
 //
 // What bounds it is HBM: it reads x and the residual and writes the sum and the output once
@@ -184,7 +184,7 @@ MOE_DEVINL F code_at_border(F zw, F amax, F a, F b) {
   return (v > border) == (b > a) ? b : a;
 }
 
-// Stores the 8 outputs of vector v (products zw; m: block_largest) of a row, where `in`.
+// Stores the 8 outputs of vector v (products zw; m: block_largest) of a row in bf16 or e4m3, where `in`.
 template <int FMT>
 MOE_DEVINL void store_vec(const float2 (&zw)[4], float m, const RowScale& r, const NormParams& p, long long row, int v,
                           bool in) {
@@ -198,7 +198,7 @@ MOE_DEVINL void store_vec(const float2 (&zw)[4], float m, const RowScale& r, con
       w[i] = pack_bf16x2(y.x, y.y);
     }
     if (in) static_cast<uint4*>(p.out)[at] = make_uint4(w[0], w[1], w[2], w[3]);
-  } else if constexpr (FMT == NORM_E4M3) {
+  } else {
     float2 y[4];
     float s = 1.f;
     const uint32_t mb = __float_as_uint(m);
@@ -230,46 +230,71 @@ MOE_DEVINL void store_vec(const float2 (&zw)[4], float m, const RowScale& r, con
       static_cast<uint2*>(p.out)[at] = make_uint2(codes_e4m3(yv), codes_e4m3(yv + 4));
       if ((threadIdx.x & 15) == 0) p.scale[at >> 4] = s;
     }
-  } else {
-    uint32_t c[8];
-    if (!r.wide) {
-      // (NaN and infinite products are in rows whose factor is 0 and whose codes are cleared below)
-      const float2 magic = make_float2(kRoundMagic, kRoundMagic);
-      float2 lo[4], hi[4];
-      uint32_t differ = 0;
+  }
+}
+
+// int8 codes of the 8 products of a vector by the estimate `factor`; `differ` is set where `above` gives others.
+// (NaN and infinite products are in rows whose factors are 0 and whose codes are not stored.)
+MOE_DEVINL uint2 codes_int8(const float2 (&zw)[4], const RowScale& r, uint32_t& differ) {
+  const float2 magic = make_float2(kRoundMagic, kRoundMagic);
+  uint32_t c[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[i] = fma2(zw[i], make_float2(r.factor, r.factor), magic);
-        hi[i] = fma2(zw[i], make_float2(r.above, r.above), magic);
-        differ |= __float_as_uint(lo[i].x) ^ __float_as_uint(hi[i].x);
-        differ |= __float_as_uint(lo[i].y) ^ __float_as_uint(hi[i].y);
-      }
-      if (differ != 0) {
+  for (int i = 0; i < 4; ++i) {
+    const float2 lo = fma2(zw[i], make_float2(r.factor, r.factor), magic), hi = fma2(zw[i], make_float2(r.above, r.above), magic);
+    c[2 * i] = __float_as_uint(lo.x);
+    c[2 * i + 1] = __float_as_uint(lo.y);
+    differ |= __float_as_uint(lo.x) ^ __float_as_uint(hi.x);
+    differ |= __float_as_uint(lo.y) ^ __float_as_uint(hi.y);
+  }
+  return make_uint2(low_bytes(c), low_bytes(c + 4));
+}
+
+// The same for every value, next to a border and in `wide` rows.  (A branch for each value: with the 8 of a
+// vector at once, or the fp64 form in a call, registers spill and 16384 x 7168 takes 159 us for 130.)
+MOE_DEVINL uint32_t code_int8_exact(float zw, const RowScale& r) {
+  if (!r.wide) {
+    const float lo = fmaf(zw, r.factor, kRoundMagic) - kRoundMagic, hi = fmaf(zw, r.above, kRoundMagic) - kRoundMagic;
+    return static_cast<uint32_t>(static_cast<int>(lo == hi ? lo : code_at_border(zw, r.amax, lo, hi)));
+  }
+  const double v = static_cast<double>(zw) * r.factor_wide;
+  double k = rint(v);
+  if (!r.clamped && fabs(v - k) > 0.5 - 1e-9)
+    k = code_at_border(static_cast<double>(zw), static_cast<double>(r.amax), k, k + (v > k ? 1.0 : -1.0));
+  return static_cast<uint32_t>(__double2int_rn(k));
+}
+MOE_DEVINL uint2 codes_int8_exact(const float2 (&zw)[4], const RowScale& r) {
+  uint32_t c[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (lo[i].x != hi[i].x)
-            lo[i].x = kRoundMagic + code_at_border(zw[i].x, r.amax, lo[i].x - kRoundMagic, hi[i].x - kRoundMagic);
-          if (lo[i].y != hi[i].y)
-            lo[i].y = kRoundMagic + code_at_border(zw[i].y, r.amax, lo[i].y - kRoundMagic, hi[i].y - kRoundMagic);
-        }
-      }
+  for (int i = 0; i < 4; ++i) {
+    c[2 * i] = code_int8_exact(zw[i].x, r);
+    c[2 * i + 1] = code_int8_exact(zw[i].y, r);
+  }
+  return make_uint2(low_bytes(c), low_bytes(c + 4));
+}
+
+// Stores the outputs of N vectors of a row, v0, v0 + step, ...; called by whole warps.  m: block_largest.
+template <int FMT, int N>
+MOE_DEVINL void store_vecs(const float2 (&zw)[N][4], const float (&m)[N], const RowScale& r, const NormParams& p, long long row,
+                           int v0, int step) {
+  if constexpr (FMT == NORM_INT8) {
+    uint2 c[N];
+    uint32_t differ = r.wide;  // (one branch for all vectors, whose steps the compiler mixes)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[2 * i] = __float_as_uint(lo[i].x);
-        c[2 * i + 1] = __float_as_uint(lo[i].y);
-      }
-    } else {
+    for (int i = 0; i < N; ++i) c[i] = codes_int8(zw[i], r, differ);
+    if (differ != 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float z = i & 1 ? zw[i / 2].y : zw[i / 2].x;
-        const double v = static_cast<double>(z) * r.factor_wide;
-        double k = rint(v);
-        if (!r.clamped && fabs(v - k) > 0.5 - 1e-9)
-          k = code_at_border(static_cast<double>(z), static_cast<double>(r.amax), k, k + (v > k ? 1.0 : -1.0));
-        c[i] = static_cast<uint32_t>(__double2int_rn(k));
-      }
+      for (int i = 0; i < N; ++i) c[i] = codes_int8_exact(zw[i], r);
     }
-    if (in) static_cast<uint2*>(p.out)[at] = r.bad ? make_uint2(0u, 0u) : make_uint2(low_bytes(c), low_bytes(c + 4));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (v0 + i * step < p.nvec)
+        static_cast<uint2*>(p.out)[row * p.nvec + v0 + i * step] = r.bad ? make_uint2(0u, 0u) : c[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int v = v0 + i * step;
+      if ((v & ~31) < p.nvec) store_vec<FMT>(zw[i], m[i], r, p, row, v, v < p.nvec);
+    }
   }
 }
 
@@ -350,11 +375,7 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(const NormParams p, con
     uint32_t amax_bits = __float_as_uint(amax);
     block_reduce(ss, amax_bits, sh_ss, sh_amax, b);
     const RowScale r = row_scale<FMT>(ss, amax_bits, p, row);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = tid + i * nt;
-      if ((v & ~31) < p.nvec) store_vec<FMT>(zw[i], m[i], r, p, row, v, v < p.nvec);
-    }
+    store_vecs<FMT, VPT>(zw, m, r, p, row, tid, nt);
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -370,14 +391,14 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormParams p) {
   const long long row = blockIdx.x, base = row * p.nvec;
   double ss = 0.0;
   float amax = 0.f;
-  float2 zw[4];
+  float2 zw[1][4];
   for (int v = threadIdx.x; v < p.nvec; v += blockDim.x) {
     uint4 z = p.x[base + v];
     if (p.res != nullptr) {
       z = add8(z, p.res[base + v]);
       if (p.res_out != nullptr) p.res_out[base + v] = z;
     }
-    products<FMT>(z, __ldg(p.w + v), zw, ss, amax);
+    products<FMT>(z, __ldg(p.w + v), zw[0], ss, amax);
   }
   uint32_t amax_bits = __float_as_uint(amax);
   block_reduce(ss, amax_bits, sh_ss, sh_amax, 0);
@@ -389,8 +410,9 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormParams p) {
       if (p.res_out != nullptr) z = p.res_out[base + v];
       else z = p.res != nullptr ? add8(p.x[base + v], p.res[base + v]) : p.x[base + v];
     }
-    products<FMT>(z, in ? __ldg(p.w + v) : z, zw, ss, amax);
-    store_vec<FMT>(zw, FMT == NORM_E4M3 ? block_largest(zw) : 0.f, r, p, row, v, in);
+    products<FMT>(z, in ? __ldg(p.w + v) : z, zw[0], ss, amax);
+    const float m[1] = {FMT == NORM_E4M3 ? block_largest(zw[0]) : 0.f};
+    store_vecs<FMT, 1>(zw, m, r, p, row, v, 0);
   }
 }
 
