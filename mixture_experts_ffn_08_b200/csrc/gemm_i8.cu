@@ -165,7 +165,7 @@ cudaError_t launch_i8_split_rows(const void* a, int64_t lda, const void* w, int6
 template <int M, int R>
 cudaError_t launch_i8_gemv(const void* a, int64_t lda, const void* w, int64_t ldw, I8Params p, cudaStream_t st) {
   // Up to eight blocks an SM, what it holds of the one-row kernel at once (of the others four to six),
-  // and no more than L2 takes in passing: 1 x 4096 x 7168 7.2 -> 6.5 us, but 2 x 14336 x 4096, where the
+  // and no more than L2 takes in passing: 1 x 4096 x 7168 7.2 -> 6.5 us in one session, but 2 x 14336 x 4096, where the
   // loads wait for it, 13.6 -> 15.7.
   p.prefetch = pdl_enabled() && cdiv(p.N, 8 * R) <= 8LL * num_sms() &&
                static_cast<long long>(p.N) * (p.K < 4096 ? p.K : 4096) <= (24LL << 20);

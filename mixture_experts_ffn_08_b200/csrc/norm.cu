@@ -24,8 +24,8 @@
 // so nothing waits for anybody but the reduction).  Six to eight instructions per channel: the sum
 // is one bf16x2 addition per pair, products and sums of squares are packed fp32 pairs, an int8
 // code is the low byte of a multiply-add onto 1.5 * 2^23.
-// Measured on B200, 16384 x 7168 with a residual: bf16 143 us (939 MB, 6.6 TB/s), e4m3 130 (825 MB,
-// 6.3 TB/s), int8 125 (822 MB, 6.6 TB/s); a plain copy runs at 6.45 TB/s.
+// Measured on B200, 16384 x 7168 with a residual: bf16 146 us (939 MB, 6.4 TB/s), e4m3 131 (825 MB,
+// 6.3 TB/s), int8 130 (822 MB, 6.3 TB/s); a plain copy runs at 6.45 TB/s.
 #include <cuda_fp8.h>
 #include <math_constants.h>
 

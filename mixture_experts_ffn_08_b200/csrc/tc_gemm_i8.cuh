@@ -14,8 +14,8 @@
 // tile while each SM's TMEM still holds two accumulators, so the epilogue of one tile runs
 // under the main loop of the next.  (At K = 1536 a tile's MMAs last only 6000 cycles and its
 // epilogue nearly as long.)  Narrower one-SM tiles spread few rows over more SMs.
-// What bounds it on B200: the power cap for large products (8192 x 14336 x 4096 in 294-311 us, the
-// tensor pipe busy 96 % of the cycles at 1.6 GHz), HBM for a decode batch's weights (6.2 TB/s).
+// What bounds it on B200: the power cap for large products (8192 x 14336 x 4096 in 287-321 us, the
+// tensor pipe busy 96 % of the cycles at 1.6 GHz), HBM for a decode batch's weights (6.2-6.6 TB/s).
 // A group's first row is a multiple of 128, not of 256: the second half of a group's last pair
 // tile may lie past the group, and then it is neither loaded nor stored.
 //
@@ -230,7 +230,7 @@ MOE_DEVINL void i8_store1(const I8Params& p, long long row, int col, float v) {
 // Direct stores of a lane's own row touch 32 lines per instruction; measured on B200 they cost
 // the 8192 x 14336 x 4096 product 16 of 345 us and the 128-expert prefill 300 of 2690 us, where
 // the TMA unit writes whole segments on its own.  (Two boxes of 64-byte rows: 16384 x 4096 x 1536 to
-// bf16 91 us against 87, medians of five.)
+// bf16 91 us against 87, medians of five runs in turn on a warm box; it takes 73 on a cool one.)
 struct I8Boxes {
   uint8_t* base;
   // A box that starts at (row, col): w0 and w1 are the halves of this lane's row.
@@ -915,7 +915,7 @@ MOE_DEVINL int4 ld_stream(const int4* p, bool in) {
 // One to four rows: nothing to share in a tile, the weights are read once whatever is done with
 // them.  A warp per R output channels, 16 codes per lane and load, integer dot products; the few
 // rows of A come from L1, each load of them used for R channels.  Many warps keep the loads in
-// flight, 64 an SM for one row (32 registers), 32 for four (52).  1 x 4096 x 7168 takes 6.5 us (4.5
+// flight, 64 an SM for one row (32 registers), 32 for four (52).  1 x 4096 x 7168 takes 7.1 us (4.1
 // TB/s), most of the rest the first bytes' way.
 template <int M, int R>
 __global__ void __launch_bounds__(256) i8_gemv_kernel(const int8_t* __restrict__ a, int64_t lda,
