@@ -171,10 +171,9 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 }
 
 // 32 lanes x 32 consecutive 32-bit columns: thread i of the warp gets lane (base+i).  The load is
-// .sync.aligned, and the step before it may have ended in a branch of some lanes (a row past the
-// last): they are joined first.
+// .sync.aligned: where the step before it ends in a branch of some lanes (a row past the last), the
+// loop joins them first (__syncwarp).  (Joined before every load instead, the e4m3 gate/up spills.)
 MOE_DEVINL void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
-  __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -189,7 +188,6 @@ MOE_DEVINL void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
 }
 
 MOE_DEVINL void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"

@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const bool v8 = ((reinterpret_cast<uintptr_t>(p.out) | (static_cast<uintptr_t>(p.ldo) * 2)) & 31) == 0;
 #pragma unroll 1
         for (int c = 0; c < BN / 2; c += 32) {
+          __syncwarp();
           uint32_t rg[32], ru[32];
           tmem_ld_32x32b_x32(tbase + c, rg);
           tmem_ld_32x32b_x32(tbase + BN / 2 + c, ru);
@@ -340,6 +341,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         float* out = static_cast<float*>(p.out) + static_cast<long long>(pair >= 0 ? pair / p.topk : 0) * p.ldo + col0;
 #pragma unroll 1
         for (int c = 0; c < BN; c += 32) {
+          __syncwarp();
           uint32_t r[32];
           tmem_ld_32x32b_x32(tbase + c, r);
           tmem_ld_wait(r);
@@ -352,6 +354,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + col0;
 #pragma unroll 1
         for (int c = 0; c < BN; c += 32) {
+          __syncwarp();
           uint32_t r[32];
           tmem_ld_32x32b_x32(tbase + c, r);
           tmem_ld_wait(r);
@@ -371,6 +374,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const bool v8 = ((reinterpret_cast<uintptr_t>(p.out) | (static_cast<uintptr_t>(p.ldo) * 4)) & 31) == 0;
 #pragma unroll 1
         for (int c = 0; c < BN; c += 32) {
+          __syncwarp();
           uint32_t r[32];
           tmem_ld_32x32b_x32(tbase + c, r);
           tmem_ld_wait(r);
@@ -389,6 +393,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         float* out = static_cast<float*>(p.out) + (item % S) * p.split_stride + row * p.ldo + col0;
 #pragma unroll 1
         for (int c = 0; c < BN; c += 16) {
+          __syncwarp();
           uint32_t r[16];
           tmem_ld_32x32b_x16(tbase + c, r);
           tmem_ld_wait(r);

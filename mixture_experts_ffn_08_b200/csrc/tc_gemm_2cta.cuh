@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + col0;
 #pragma unroll 1
         for (int c = 0; c < BN / 2; c += 32) {
+          __syncwarp();
           uint32_t rg[32], ru[32];
           tmem_ld_32x32b_x32(tbase + c, rg);
           tmem_ld_32x32b_x32(tbase + BN / 2 + c, ru);
@@ -439,6 +440,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         float* out = static_cast<float*>(p.out) + row * p.ldo + col0;
 #pragma unroll 1
         for (int c = 0; c < BN; c += 32) {
+          __syncwarp();
           uint32_t r[32];
           tmem_ld_32x32b_x32(tbase + c, r);
           tmem_ld_wait(r);
@@ -453,6 +455,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + col0;
 #pragma unroll 1
         for (int c = 0; c < BN; c += 32) {
+          __syncwarp();
           uint32_t r[32];
           tmem_ld_32x32b_x32(tbase + c, r);
           tmem_ld_wait(r);

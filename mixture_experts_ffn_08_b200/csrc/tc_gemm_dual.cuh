@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(kDualThreads, 1)
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(out_base) + orow * ldo + col0;
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
+            __syncwarp();
             uint32_t rg[32], ru[32];
             tmem_ld_32x32b_x32(tbase + c, rg);
             tmem_ld_32x32b_x32(tbase + 128 + c, ru);
@@ -394,6 +395,7 @@ __global__ void __launch_bounds__(kDualThreads, 1)
           bool range_ok = true;
 #pragma unroll 1
           for (int c = 0; c < 256; c += 32) {
+            __syncwarp();
             uint32_t r[32];
             tmem_ld_32x32b_x32(tbase + c, r);
             tmem_ld_wait(r);
@@ -415,6 +417,7 @@ __global__ void __launch_bounds__(kDualThreads, 1)
           float* out = static_cast<float*>(out_base) + orow * ldo + col0;
 #pragma unroll 1
           for (int c = 0; c < 256; c += 32) {
+            __syncwarp();
             uint32_t r[32];
             tmem_ld_32x32b_x32(tbase + c, r);
             tmem_ld_wait(r);

@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + col0;
 #pragma unroll 1
         for (int c = 0; c < BN; c += 32) {
+          __syncwarp();
           uint32_t r[32];
           tmem_ld_32x32b_x32(tbase + c, r);
           tmem_ld_wait(r);

@@ -543,6 +543,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         float* out = static_cast<float*>(p.out) + row * p.ldo + col0;
 #pragma unroll 1
         for (int c = 0; c < Cfg::OUT_COLS; c += 32) {
+          __syncwarp();
           uint32_t rg[32], ru[32];
           tmem_ld_32x32b_x32(tbase + c, rg);
           tmem_ld_32x32b_x32(tbase + BN / 2 + c, ru);
@@ -564,6 +565,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         // 64 columns at a time: one wait and one fence for a box of 16-bit outputs
 #pragma unroll 1
         for (int c = 0; c < BN; c += 64) {
+          __syncwarp();
           uint32_t r[2][32];
 #pragma unroll
           for (int j = 0; j < 2; ++j) tmem_ld_32x32b_x32(tbase + c + 32 * j, r[j]);
@@ -848,6 +850,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const float sa = row_sh[row];
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
+        __syncwarp();
         uint32_t r[32];
         tmem_ld_32x32b_x32(tbase + c, r);
         tmem_ld_wait(r);
